@@ -14,6 +14,9 @@
  *      (jano_active_attention, or jano_active_attention_split for due sets
  *      too small to fill the GPU), their outputs going back to their token
  *      rows.
+ * Beside them: the rotary positions that Q and K take before the cache, and
+ * a cache in pages shared by several generations (jano_axis_rope,
+ * jano_rope_scatter, jano_paged_append, jano_paged_attention).
  *
  * Conventions shared by every entry point
  *   - All pointers named *device* below are device pointers on the current
@@ -422,6 +425,177 @@ JANO_API jano_status jano_fft_scores(const float *x, int C, const jano_geom *g, 
  * ---------------------------------------------------------------------- */
 JANO_API jano_status jano_stream_sum(const float *x, long long n, float *partial, int n_partial,
                                      void *stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions with several axes (frame, row, column).  The attention
+ * takes Q and K after any positional encoding; these entry points apply the
+ * rotary one, alone or on the way into a cache.
+ *
+ * A head's first rot = axes[0] + axes[1] + axes[2] columns form rot / 2
+ * slots, axes[0] / 2 of them for axis 0, and so on.  Slot s pairs the columns
+ * (2s, 2s + 1) (halves = 0) or (s, s + rot / 2) (halves = 1) and turns them
+ * by the angle of the token's coordinate p on the slot's axis:
+ *
+ *   (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos),
+ *   angle = p * theta^(-2 i / axes[a])      i: the slot's number on its axis a
+ *         = p * theta^(-2 s / rot)          shared_freq: one series over all slots
+ *
+ * in fp32, one rounding to BF16; columns from rot on are kept bit for bit.
+ * cos and sin come from a table of (cos, sin) fp32 pairs, n_pos[a] positions
+ * x axes[a] / 2 slots for axis 0, then axis 1, then axis 2, made once by
+ * jano_rope_table (angles in fp64) or by the caller.
+ *
+ * A row's coordinates are coords[r][0..2], or, with coords NULL, those of its
+ * token id t on the token grid: t / (grid_w * grid_h), t / grid_w % grid_h,
+ * t % grid_w.
+ *
+ * Limits of the configuration: axes even and >= 0, 0 < rot <= d,
+ * n_pos >= 1, d a multiple of 8 up to 1024; with halves rot a multiple of 16
+ * (JANO_EUNSUPPORTED); without coords grid_h, grid_w >= 1 (JANO_EINVAL).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    int axes[3];           /* columns per axis                             */
+    int n_pos[3];          /* positions per axis that the table holds      */
+    int grid_h, grid_w;    /* token grid of the ids                        */
+    int halves;            /* pairing, see above                           */
+} jano_rope_cfg;
+
+/* Floats of the table (twice its entries); 0 for a bad configuration. */
+JANO_API size_t jano_rope_table_floats(const jano_rope_cfg *c);
+
+/* Fills table (device fp32, jano_rope_table_floats, 8-byte aligned).
+ * theta > 0 and finite. */
+JANO_API jano_status jano_rope_table(const jano_rope_cfg *c, double theta, int shared_freq,
+                                     float *table, void *stream);
+
+/* ------------------------------------------------------------------------
+ * jano_axis_rope -- out[r] = x[r] rotated, for r < n_rows.
+ *
+ * x, out   device BF16 rows of heads * d, x_ld / out_ld elements apart
+ *          (multiples of 8, at least heads * d); 16-byte aligned.  They may
+ *          be the same buffer (with the same row distance), else they must
+ *          not overlap.
+ * ids      device int32 [n_rows], the token ids (any order, repeats
+ *          allowed), or NULL (row r is token r).  Not read with coords.
+ * coords   device int32 [n_rows][3] or NULL.
+ * A row with a negative id or a coordinate outside [0, n_pos[a]) (of an axis
+ * that has slots) raises JANO_EINDEX on the device error word and is not
+ * written.  n_rows == 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+JANO_API jano_status jano_axis_rope(const void *x, long long x_ld, const int32_t *ids,
+                                    const int32_t *coords, int n_rows, int heads, int d,
+                                    const jano_rope_cfg *c, const float *table, void *out,
+                                    long long out_ld, void *stream);
+
+/* ------------------------------------------------------------------------
+ * jano_rope_scatter -- jano_kv_scatter with the rotation on the way, and the
+ * queries rotated in the same launch:
+ *   k_cache[idx[i]] = R(k[i]), v_cache[idx[i]] = v[i], q_out[i] = R(q[i]).
+ *
+ * q, q_out  rows of heads * d, or both NULL; q_out may be q (same row
+ *           distance).
+ * k, v      rows of kv_heads * d; row distances as above, so all three may
+ *           be columns of one fused projection buffer.
+ * idx       device int32 [n_act], strictly ascending in [0, n_tokens); also
+ *           the token ids of the coordinates (unless coords are given).
+ * k_cache, v_cache  device BF16 [n_tokens][kv_heads][d].
+ * A row whose id or coordinate is bad raises JANO_EINDEX and is skipped (its
+ * q_out row too).
+ * ---------------------------------------------------------------------- */
+JANO_API jano_status jano_rope_scatter(const void *q, long long q_ld, const void *k, long long k_ld,
+                                       const void *v, long long v_ld, const int32_t *idx,
+                                       const int32_t *coords, int n_act, int heads, int kv_heads,
+                                       int d, const jano_rope_cfg *c, const float *table,
+                                       void *q_out, long long q_out_ld, void *k_cache,
+                                       void *v_cache, int n_tokens, void *stream);
+
+/* ------------------------------------------------------------------------
+ * A KV cache in pages shared by several sequences (generations).  The pool
+ * holds n_pages pages of page_size places; sequence s has its position j at
+ * place j % page_size of page page_table[s][j / page_size].  K and V lie at
+ * the same places of two buffers with the same strides, so token-major
+ * ([page][place][head][d]) and head-major ([page][head][place][d]) pools, and
+ * pools with K and V inside one allocation, are all described.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    void *k, *v;           /* device BF16, 16-byte aligned                 */
+    int n_pages;
+    int page_size;         /* 16, 32, 64, 128 or 256                       */
+    int kv_heads, d;
+    long long page_stride, token_stride, head_stride;   /* elements, multiples of 8 */
+} jano_page_pool;
+
+/* The sequences of a call.  Rows (of q, k, v, out) are packed: sequence s
+ * owns the rows cu_rows[s] .. cu_rows[s+1]; rows from cu_rows[n_seqs] on
+ * belong to none and are left alone. */
+typedef struct {
+    const int32_t *page_table;   /* device [n_seqs][max_pages]; entries past a sequence's length are not read */
+    const int32_t *seq_lens;     /* device [n_seqs], positions in the cache (those of the call included) */
+    const int32_t *cu_rows;      /* device [n_seqs + 1], ascending from 0  */
+    int n_seqs, max_pages;
+} jano_page_seqs;
+
+/* ------------------------------------------------------------------------
+ * jano_paged_append -- write new K/V rows into the pages of their sequences,
+ * K rotated on the way, and the queries rotated in the same launch: with s
+ * the sequence of row r and p = pos[r],
+ *   K page slot of (s, p) = R(k[r]), V page slot = v[r], q_out[r] = R(q[r]).
+ *
+ * pos      device int32 [n_rows], strictly ascending within a sequence, in
+ *          [0, seq_lens[s]).
+ * c, table the rotation, or both NULL: K and Q are copied.
+ * coords   device int32 [n_rows][3] or NULL (from pos and the grid).
+ * grids    device int32 [n_seqs][2], each sequence's (rows, columns), or
+ *          NULL (grid_h, grid_w for all).
+ * q, q_out, k, v, row distances: as jano_rope_scatter; the new rows must not
+ * overlap the pool.  d a multiple of 8.
+ * A row whose position, page id or coordinate is bad, or that meets a
+ * cu_rows that does not rise from 0, raises JANO_EINDEX; such rows are
+ * skipped (their q_out rows too).
+ * A page written in a call belongs to one sequence of it: two rows that
+ * meet in the same place through a shared page race.
+ * ---------------------------------------------------------------------- */
+JANO_API jano_status jano_paged_append(const jano_page_pool *pool, const jano_page_seqs *seqs,
+                                       const void *q, long long q_ld, const void *k, long long k_ld,
+                                       const void *v, long long v_ld, const int32_t *pos,
+                                       const int32_t *coords, const int32_t *grids, int n_rows,
+                                       int heads, const jano_rope_cfg *c, const float *table,
+                                       void *q_out, long long q_out_ld, void *stream);
+
+/* ------------------------------------------------------------------------
+ * jano_paged_attention -- attention of a chunk of rows of each sequence over
+ * its pages:
+ *   out[r, h] = sum_{j < L_r} softmax_j(scale * q[r, h] . k_j) v_j,
+ *   L_r = min(seq_lens[s], limits[r])  (limits NULL: seq_lens[s]),
+ * k_j, v_j position j of r's sequence s, head h / (heads / kv_heads).  A row
+ * that sees nothing (L_r <= 0) gives 0.  limits[r] = pos[r] + 1 is the causal
+ * mask, (frame + 1) * tokens per frame the mask by frames; any values do.
+ *
+ * q, out   device BF16 rows of heads * d, q_ld / out_ld elements apart
+ *          (multiples of 8); 16-byte aligned; no overlap.
+ * heads    a multiple of kv_heads, at most 128 per K/V head.
+ * d        64 or 128 (the pool's).
+ * max_rows, max_len  upper bounds of a sequence's rows and length (grid and
+ *          split choice only); a sequence above either, or with a bad length
+ *          or cu_rows, raises JANO_EINDEX and its rows are not written.
+ * n_split  CTAs that share one query tile's keys: 1, 2, 4, 8 or 16 (a
+ *          thread-block cluster; 16 falls to 8 where the device cannot run
+ *          such clusters), or 0 for the library's choice.
+ * A page id outside the pool raises JANO_EINDEX and reads as zeros.  K and V
+ * at positions below the sequence's length must be finite; places past it
+ * may hold anything.  BF16 in, fp32 accumulation and softmax, BF16 out.
+ * Deterministic.  No workspace.
+ * ---------------------------------------------------------------------- */
+JANO_API jano_status jano_paged_attention(const jano_page_pool *pool, const jano_page_seqs *seqs,
+                                          const void *q, long long q_ld, const int32_t *limits,
+                                          int n_rows, int max_rows, int max_len, int heads,
+                                          float scale, int n_split, void *out, long long out_ld,
+                                          void *stream);
+
+/* The split jano_paged_attention takes for n_split = 0 on a device of
+ * sm_count SMs (host only); 1 on invalid arguments. */
+JANO_API int jano_paged_attention_splits_on(int n_rows, int max_rows, int max_len, int n_seqs,
+                                            int heads, int kv_heads, int sm_count);
 
 /* Synchronises `stream`, returns the first device-side error recorded on the
  * current device since the last call (JANO_OK if none) and clears it. */

@@ -266,6 +266,169 @@ jano_status jano_stream_sum(const float* x, long long n, float* partial, int n_p
     return from_cuda(launch_stream_sum(x, n, partial, n_partial, err, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+jano_status check_rope(const jano_rope_cfg* c, int d, bool have_coords) {
+    if (!c) return JANO_EINVAL;
+    long long rot = 0, entries = 0;
+    for (int x = 0; x < 3; ++x) {
+        if (c->axes[x] < 0 || c->axes[x] % 2 || c->n_pos[x] < 1) return JANO_EINVAL;
+        rot += c->axes[x];
+        entries += (long long)c->n_pos[x] * (c->axes[x] / 2);
+    }
+    if (rot < 1 || rot > d) return JANO_EINVAL;
+    if (!have_coords && (c->grid_h < 1 || c->grid_w < 1)) return JANO_EINVAL;
+    if (entries > INT_MAX / 2 || (c->halves && rot % 16)) return JANO_EUNSUPPORTED;
+    return JANO_OK;
+}
+
+// A row buffer: rows of `width` elements, ld apart.
+jano_status check_rows(const void* p, long long ld, long long width) {
+    if (!p) return JANO_EINVAL;
+    if (ld < width) return JANO_ESHAPE;
+    if (ld % 8) return JANO_EUNSUPPORTED;
+    return aligned16(p) ? JANO_OK : JANO_EALIGN;
+}
+
+bool head_dim_ok(int d) { return d % 8 == 0 && d <= 1024; }
+
+jano_status check_pool(const jano_page_pool* p, const jano_page_seqs* s) {
+    if (!p || !s || !p->k || !p->v || !s->page_table || !s->seq_lens || !s->cu_rows) return JANO_EINVAL;
+    if (p->n_pages < 1 || p->kv_heads < 1 || p->d < 1 || s->n_seqs < 1 || s->max_pages < 1) return JANO_EINVAL;
+    const int z = p->page_size;
+    if (z != 16 && z != 32 && z != 64 && z != 128 && z != 256) return JANO_EUNSUPPORTED;
+    const long long most = 1ll << 38;          // a stride in bytes stays below 2^40
+    for (const long long st : {p->page_stride, p->token_stride, p->head_stride}) {
+        if (st < p->d) return JANO_ESHAPE;
+        if (st % 8 || st >= most) return JANO_EUNSUPPORTED;
+    }
+    if ((long long)s->max_pages * z > INT_MAX) return JANO_EUNSUPPORTED;
+    if (!aligned16(p->k) || !aligned16(p->v)) return JANO_EALIGN;
+    return JANO_OK;
+}
+
+// The queries, keys and values of an append or scatter.
+jano_status check_qkv(const RopeCacheCall& r) {
+    if (r.n_rows < 0 || r.heads < 1 || r.kv_heads < 1 || r.d < 1) return JANO_EINVAL;
+    if (!head_dim_ok(r.d)) return JANO_EUNSUPPORTED;
+    const long long q_w = (long long)r.heads * r.d, k_w = (long long)r.kv_heads * r.d;
+    if (q_w > INT_MAX || k_w > INT_MAX) return JANO_EUNSUPPORTED;
+    if (!r.ids || (r.q != nullptr) != (r.q_out != nullptr)) return JANO_EINVAL;
+    jano_status st;
+    if (r.q) {
+        if ((st = check_rows(r.q, r.q_ld, q_w)) != JANO_OK) return st;
+        if ((st = check_rows(r.q_out, r.q_out_ld, q_w)) != JANO_OK) return st;
+    }
+    if ((st = check_rows(r.k, r.k_ld, k_w)) != JANO_OK) return st;
+    return check_rows(r.v, r.v_ld, k_w);
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+}  // namespace
+
+size_t jano_rope_table_floats(const jano_rope_cfg* c) {
+    if (check_rope(c, INT_MAX, true) != JANO_OK) return 0;
+    size_t n = 0;
+    for (int x = 0; x < 3; ++x) n += (size_t)c->n_pos[x] * c->axes[x];
+    return n;
+}
+
+jano_status jano_rope_table(const jano_rope_cfg* c, double theta, int shared_freq, float* table, void* stream) {
+    const jano_status s = check_rope(c, INT_MAX, true);
+    if (s != JANO_OK) return s;
+    if (!table || !(theta > 0.0) || !std::isfinite(theta)) return JANO_EINVAL;
+    if (!aligned8(table)) return JANO_EALIGN;
+    return from_cuda(launch_rope_table(*c, theta, shared_freq, table, static_cast<cudaStream_t>(stream)));
+}
+
+jano_status jano_axis_rope(const void* x, long long x_ld, const int32_t* ids, const int32_t* coords, int n_rows,
+                           int heads, int d, const jano_rope_cfg* c, const float* table, void* out,
+                           long long out_ld, void* stream) {
+    if (n_rows < 0 || heads < 1 || d < 1) return JANO_EINVAL;
+    const jano_status cs = check_rope(c, d, coords != nullptr);
+    if (cs != JANO_OK) return cs;
+    if (!head_dim_ok(d) || (long long)heads * d > INT_MAX) return JANO_EUNSUPPORTED;
+    if (n_rows == 0) return JANO_OK;
+    if (!table) return JANO_EINVAL;
+    jano_status s = check_rows(x, x_ld, (long long)heads * d);
+    if (s == JANO_OK) s = check_rows(out, out_ld, (long long)heads * d);
+    if (s != JANO_OK) return s;
+    if (!aligned8(table)) return JANO_EALIGN;
+    int* err = device_error_word();
+    if (!err) return JANO_ECUDA;
+    return from_cuda(launch_axis_rope(x, x_ld, coords ? nullptr : ids, coords, n_rows, heads, d, *c, table, out,
+                                      out_ld, err, static_cast<cudaStream_t>(stream)));
+}
+
+jano_status jano_rope_scatter(const void* q, long long q_ld, const void* k, long long k_ld, const void* v,
+                              long long v_ld, const int32_t* idx, const int32_t* coords, int n_act, int heads,
+                              int kv_heads, int d, const jano_rope_cfg* c, const float* table, void* q_out,
+                              long long q_out_ld, void* k_cache, void* v_cache, int n_tokens, void* stream) {
+    if (n_act < 0 || n_tokens < 1 || heads < 1 || kv_heads < 1 || d < 1) return JANO_EINVAL;
+    const jano_status cs = check_rope(c, d, coords != nullptr);
+    if (cs != JANO_OK) return cs;
+    if (n_act == 0) return JANO_OK;
+    RopeCacheCall r{q, k, v, q_ld, k_ld, v_ld, idx, coords, nullptr, n_act, heads, kv_heads, d, c, table,
+                    q_out, q_out_ld, k_cache, v_cache, 0, (long long)kv_heads * d, d, n_tokens, 0, 0, nullptr};
+    const jano_status s = check_qkv(r);
+    if (s != JANO_OK) return s;
+    if (!table || !k_cache || !v_cache) return JANO_EINVAL;
+    if (!aligned8(table) || !aligned16(k_cache) || !aligned16(v_cache)) return JANO_EALIGN;
+    int* err = device_error_word();
+    if (!err) return JANO_ECUDA;
+    return from_cuda(launch_rope_cache(r, err, static_cast<cudaStream_t>(stream)));
+}
+
+jano_status jano_paged_append(const jano_page_pool* pool, const jano_page_seqs* seqs, const void* q, long long q_ld,
+                              const void* k, long long k_ld, const void* v, long long v_ld, const int32_t* pos,
+                              const int32_t* coords, const int32_t* grids, int n_rows, int heads,
+                              const jano_rope_cfg* c, const float* table, void* q_out, long long q_out_ld,
+                              void* stream) {
+    if (n_rows < 0) return JANO_EINVAL;
+    if (n_rows == 0) return JANO_OK;
+    jano_status s = check_pool(pool, seqs);
+    if (s != JANO_OK) return s;
+    if ((c != nullptr) != (table != nullptr)) return JANO_EINVAL;
+    if (c && (s = check_rope(c, pool->d, coords || grids)) != JANO_OK) return s;
+    if (c && !aligned8(table)) return JANO_EALIGN;
+    RopeCacheCall r{q, k, v, q_ld, k_ld, v_ld, pos, coords, grids, n_rows, heads, pool->kv_heads, pool->d, c, table,
+                    q_out, q_out_ld, pool->k, pool->v, pool->page_stride, pool->token_stride, pool->head_stride, 0,
+                    pool->n_pages, pool->page_size, seqs};
+    if ((s = check_qkv(r)) != JANO_OK) return s;
+    int* err = device_error_word();
+    if (!err) return JANO_ECUDA;
+    return from_cuda(launch_rope_cache(r, err, static_cast<cudaStream_t>(stream)));
+}
+
+jano_status jano_paged_attention(const jano_page_pool* pool, const jano_page_seqs* seqs, const void* q, long long q_ld,
+                                 const int32_t* limits, int n_rows, int max_rows, int max_len, int heads,
+                                 float scale, int n_split, void* out, long long out_ld, void* stream) {
+    if (n_rows < 0 || max_rows < 0 || max_len < 0 || heads < 1) return JANO_EINVAL;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return JANO_EINVAL;
+    if (n_split < 0 || n_split > 16 || (n_split & (n_split - 1))) return JANO_EINVAL;
+    if (n_rows == 0) return JANO_OK;
+    jano_status s = check_pool(pool, seqs);
+    if (s != JANO_OK) return s;
+    if (pool->d != 64 && pool->d != 128) return JANO_EUNSUPPORTED;
+    if (heads % pool->kv_heads) return JANO_ESHAPE;
+    if (heads / pool->kv_heads > 128 || pool->kv_heads > 65535) return JANO_EUNSUPPORTED;
+    if (q_ld >= (1ll << 38) || (long long)heads * pool->d > INT_MAX) return JANO_EUNSUPPORTED;
+    if ((s = check_rows(q, q_ld, (long long)heads * pool->d)) != JANO_OK) return s;
+    if ((s = check_rows(out, out_ld, (long long)heads * pool->d)) != JANO_OK) return s;
+    int* err = device_error_word();
+    if (!err) return JANO_ECUDA;
+    const PagedAttentionCall c{pool, seqs, q, q_ld, limits, n_rows, max_rows < 1 ? 1 : max_rows, max_len, heads,
+                               scale, n_split, out, out_ld};
+    return from_cuda(launch_paged_attention(c, err, static_cast<cudaStream_t>(stream)));
+}
+
+int jano_paged_attention_splits_on(int n_rows, int max_rows, int max_len, int n_seqs, int heads, int kv_heads,
+                                   int sm_count) {
+    if (n_rows < 1 || max_rows < 1 || max_len < 1 || n_seqs < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads ||
+        heads / kv_heads > 128 || sm_count < 1)
+        return 1;
+    return paged_split_count(n_rows, max_rows, max_len, n_seqs, heads, kv_heads, sm_count);
+}
+
 jano_status jano_get_device_error(void* stream) {
     int* err = device_error_word();
     if (!err) return JANO_ECUDA;

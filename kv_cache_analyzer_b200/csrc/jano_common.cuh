@@ -87,6 +87,45 @@ cudaError_t launch_projection(const void* x, int n_x, const int32_t* gather, int
                               int n, int k, int n_seg, const ProjSeg* segs, int* err,
                               cudaStream_t st);
 int projection_tile_n(int n, int seg_w, int n_seg);
+
+// Rotary positions with several axes: the table, rows alone, and rows on the
+// way into a cache (seqs NULL: the token-ordered cache, n_tokens rows; else
+// the pool's pages).  cfg NULL: no rotation.  q NULL: no queries.
+struct RopeCacheCall {
+    const void *q, *k, *v;
+    long long q_ld, k_ld, v_ld;              // elements between rows
+    const int32_t *ids, *coords, *grids;
+    int n_rows, heads, kv_heads, d;
+    const jano_rope_cfg* cfg;
+    const float* table;
+    void* q_out;
+    long long q_out_ld;
+    void *k_cache, *v_cache;
+    long long page_stride, token_stride, head_stride;   // elements
+    int n_tokens, n_pages, page_size;
+    const jano_page_seqs* seqs;
+};
+cudaError_t launch_rope_table(const jano_rope_cfg& c, double theta, int shared_freq, float* table, cudaStream_t st);
+cudaError_t launch_axis_rope(const void* x, long long x_ld, const int32_t* ids, const int32_t* coords, int n_rows,
+                             int heads, int d, const jano_rope_cfg& c, const float* table, void* out,
+                             long long out_ld, int* err, cudaStream_t st);
+cudaError_t launch_rope_cache(const RopeCacheCall& r, int* err, cudaStream_t st);
+
+struct PagedAttentionCall {
+    const jano_page_pool* pool;
+    const jano_page_seqs* seqs;
+    const void* q;
+    long long q_ld;
+    const int32_t* limits;
+    int n_rows, max_rows, max_len, heads;
+    float scale;
+    int n_split;                             // CTAs per (query tiles, K/V head); 0: paged_split_count
+    void* out;
+    long long out_ld;
+};
+cudaError_t launch_paged_attention(const PagedAttentionCall& c, int* err, cudaStream_t st);
+int paged_split_count(int n_rows, int max_rows, int max_len, int n_seqs, int heads, int kv_heads, int sms);
+
 cudaError_t launch_random_scores(int n, uint64_t seed, float* scores, cudaStream_t st);
 cudaError_t launch_stream_sum(const float* x, long long n, float* partial, int n_partial, int* err,
                               cudaStream_t st);
