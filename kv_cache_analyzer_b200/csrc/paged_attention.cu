@@ -31,7 +31,9 @@
 // 8 TMA producer, 9 MMA issuer, 10 clears V rows past the visible length
 // (stale pages may hold NaN there, and 0 * NaN would reach O), 11 idle.  A
 // 128-key tile is gathered page by page: one box of min(page_size, 128) rows
-// x 64 columns per page and panel, page ids read by the producer's lanes.
+// x 64 columns per page and panel.  The producer and the MMA issuer each run as
+// one elected thread: elect.sync lets the compiler keep their operands in
+// uniform registers, which halved the MMA thread's time per key tile.
 // The pool's map has page, head and token strides of its own, so token-major
 // and head-major pools, and K and V inside one allocation, read alike.
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [384,384+d); P_i is
@@ -63,8 +65,11 @@ constexpr int kRegsLaunch = 168;
 constexpr int kRegsSoftmax = 208;
 constexpr int kRegsIssue = 80;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
+static_assert(2 * kRegsSoftmax + kRegsIssue <= 512, "sub-partition register file");
 constexpr uint32_t kPanel = 128 * 128;       // bytes of one 128-row x 64-column panel
+constexpr int kSoftmaxWarps = 8;
 constexpr int kMaxSplit = 16;
+constexpr int kMaxBoxes = 8;         // pages of 16 rows in a 128-key tile
 constexpr long long kWaitLimit = 1ll << 31;  // cycles (~1 s)
 
 template <int HD>
@@ -118,16 +123,13 @@ struct Ctl {
     volatile int* abort;
     int* err;
     __device__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
-    // Waiting threads sleep until the phase completes; the MMA thread polls
+    // Waiting threads sleep until the phase completes; the MMA warp polls
     // (its waits sit on every key tile's critical path).
-    __device__ bool wait(int i, uint32_t parity, bool spin = false) const {
-        auto poll = [&]() {
-            return spin ? ptx::mbar_try_wait(bar(i), parity) : ptx::mbar_try_wait_sleep(bar(i), parity);
-        };
-        if (poll()) return true;
+    __device__ bool wait(int i, uint32_t parity) const {
+        if (ptx::mbar_try_wait_sleep(bar(i), parity)) return true;
         const long long t0 = clock64();
         for (;;) {
-            if (poll()) return true;
+            if (ptx::mbar_try_wait_sleep(bar(i), parity)) return true;
             if (*abort) return false;
             if (clock64() - t0 > kWaitLimit) {
                 *abort = 1;
@@ -135,6 +137,19 @@ struct Ctl {
                 return false;
             }
         }
+    }
+    __device__ bool poll(int i, uint32_t parity) const {
+        if (ptx::mbar_try_wait(bar(i), parity)) return true;
+        const long long t0 = clock64();
+        while (!ptx::mbar_try_wait(bar(i), parity)) {
+            if (*abort) return false;
+            if (clock64() - t0 > kWaitLimit) {
+                *abort = 1;
+                raise_error(err, JANO_ETIMEOUT);
+                return false;
+            }
+        }
+        return true;
     }
     // Warp-uniform: the .sync.aligned operations that follow never diverge.
     __device__ bool warp_wait(int i, uint32_t parity) const {
@@ -144,6 +159,8 @@ struct Ctl {
     }
 };
 
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1, int c2,
@@ -152,6 +169,32 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4, %5, %6}], [%2];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
+}
+// Shared-memory operand descriptors as two words, so that stepping through a
+// tile is one 32-bit add: the low word holds address / 16 and the leading
+// offset, the high word (stride 1024, 128-byte swizzle) is the same for all.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// (the mask drops the CTA rank that a shared address carries inside a cluster)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+    return ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
+                 ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool acc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+                 ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+// One lane of the converged warp, chosen by the hardware: unlike lane == 0 it
+// tells the compiler that a single thread runs what follows.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
     float2 v;
@@ -229,8 +272,10 @@ __device__ __forceinline__ float exp64(const uint32_t (&s)[64], int valid, float
 // One key tile of one tile row (see the file comment): S from TMEM, maximum,
 // lazy rescale of O, P back as BF16.  `valid`: keys of the tile this row sees.
 template <int HD, bool kMask>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t tP, bool first, int valid, float c,
-                                             float& m, float& l, uint32_t bar_half) {
+__device__ __forceinline__ void softmax_tile(uint32_t tS, int valid, float c, float& m, float& l, uint32_t bar_half) {
+    constexpr uint32_t kO = Layout<HD>::tO(0) - Layout<HD>::tS(0);      // the same for both streams
+    static_assert(Layout<HD>::tO(1) - Layout<HD>::tS(1) == kO, "O lies at one distance from S");
+    const uint32_t tO = tS + kO, tP = tS + Layout<HD>::tP;
     uint32_t s[128];
     ptx::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
     ptx::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
@@ -244,7 +289,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, uint32_t 
     const bool want = mxs > m + 8.0f;
     if (__any_sync(0xFFFFFFFFu, want)) {
         const float m_new = want ? mxs : m;
-        if (!first) {
+        // nothing to rescale while no row of the warp has seen a key
+        if (__any_sync(0xFFFFFFFFu, m > -INFINITY)) {
             const float alpha = want ? ptx::ex2(m - m_new) : 1.0f;
             l *= alpha;
 #pragma unroll
@@ -333,6 +379,76 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int x, bool report) {
     return p;
 }
 
+// Parts of a tile row: one per CTA of the cluster, two (the streams) in the
+// single form.  With M the largest m and w = 2^(m - M),
+//   out = sum w O / sum w l,   summed in a fixed order;
+// one softmax warp per row, the rows dealt over the cluster's.  The plan is
+// read again from shared memory, so nothing of it is held through the loops.
+template <int HD>
+__device__ __forceinline__ void merge_rows(const Args& a) {
+    using L = Layout<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const volatile int* plan = reinterpret_cast<const volatile int*>(smem_raw + (base - raw) + L::kMisc + 16);
+    const int row0 = plan[1], rows0 = plan[2], rows1 = plan[3];
+    const bool single = rows1 == 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_split = (int)gridDim.z;
+    constexpr int E = HD / 32;                     // columns per lane
+    const int packed0 = rows0 * a.group, total = packed0 + rows1 * a.group;
+    const int parts = single ? 2 * n_split : n_split;
+    for (int r = (int)blockIdx.z * kSoftmaxWarps + warp; r < total; r += n_split * kSoftmaxWarps) {
+        const int tile = r >= packed0, p = tile ? r - packed0 : r;
+        // lane = part: its address, weight and share of the sum
+        const int z = single ? lane >> 1 : lane, st = single ? lane & 1 : tile;
+        uint32_t row_addr = 0;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < parts) {
+            const uint32_t peer = ptx::mapa_shared(base, (uint32_t)z);
+            ml = ld_cluster_f2(peer + L::kMl + (st * BM + p) * 8);
+            row_addr = peer + (st * BM + p) * L::kRow * 4;
+        }
+        if (__any_sync(0xFFFFFFFFu, ml.y < 0.f)) continue;     // a part is missing: JANO_ETIMEOUT was raised
+        float M = ml.x, sum;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+        // a part without visible keys has m = -inf, l = 0 and no O
+        const float w = ml.y != 0.f ? ptx::ex2(ml.x - M) : 0.f;
+        sum = w * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int c = 0; c < parts; ++c) {
+            const float wc = __shfl_sync(0xFFFFFFFFu, w, c);
+            const uint32_t ac = __shfl_sync(0xFFFFFFFFu, row_addr, c);
+            if (wc != 0.f) {
+                if constexpr (E == 4) {
+                    const float4 o = ld_cluster_f4(ac + lane * 16);
+                    acc[0] = fmaf(wc, o.x, acc[0]);
+                    acc[1] = fmaf(wc, o.y, acc[1]);
+                    acc[2] = fmaf(wc, o.z, acc[2]);
+                    acc[3] = fmaf(wc, o.w, acc[3]);
+                } else {
+                    const float2 o = ld_cluster_f2(ac + lane * 8);
+                    acc[0] = fmaf(wc, o.x, acc[0]);
+                    acc[1] = fmaf(wc, o.y, acc[1]);
+                }
+            }
+        }
+        const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+        __nv_bfloat16* dst = a.out + (long long)(row0 + tile * a.tile_rows + p / a.group) * a.out_ld +
+                             ((int)blockIdx.y * a.group + p % a.group) * HD + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(ptx::pack_bf16(acc[0] * inv, acc[1] * inv), ptx::pack_bf16(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = ptx::pack_bf16(acc[0] * inv, acc[1] * inv);
+    }
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -393,9 +509,13 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    const int seq = plan_slot[0], row0 = plan_slot[1], rows0 = plan_slot[2], rows1 = plan_slot[3];
-    const int seen = max(plan_slot[4], 0);
+    // warp reductions tell the compiler that these are the same in every lane:
+    // branches on them are uniform, and the MMAs take their descriptors and
+    // addresses from uniform registers
+    const uint32_t tmem = uniform(*tmem_slot);
+    const int seq = uniform(plan_slot[0]), row0 = uniform(plan_slot[1]);
+    const int rows0 = uniform(plan_slot[2]), rows1 = uniform(plan_slot[3]);
+    const int seen = uniform(max(plan_slot[4], 0));
     const bool single = rows1 == 0;
     // this CTA's key tiles [kt0, kt0 + n); n steps per stream in the pair
     // form, ceil(n / 2) and floor(n / 2) in the single form
@@ -410,7 +530,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       ptx::setmaxnreg_dec<kRegsIssue>();
       if (warp == 8 && n > 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t q_bytes = (uint32_t)(a.tile_rows * a.group * 128 * L::kPanels);
             ptx::mbar_arrive_expect_tx(ctl.bar(L::bQFull), single ? q_bytes : 2 * q_bytes);
             for (int p = 0; p < L::kPanels; ++p) {
@@ -419,45 +539,54 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                     ptx::tma_load_3d(base + L::kQ1 + p * kPanel, &tmQ, ctl.bar(L::bQFull), p * 64, head * a.group,
                                      row0 + a.tile_rows);
             }
-        }
-        const int page_rows = 1 << a.page_shift;
-        const int box_rows = min(page_rows, BN);
-        const int32_t* pages = a.table + (long long)seq * a.max_pages;
-        int issued = 0;
-        for (int i = 0; i < 2 * n; ++i) {
-            bool is_v;
-            const int g = order.tile(i, is_v);
-            const int key0 = (kt0 + g) * BN;
-            const int live = min(seen - key0, BN);
-            const int boxes = (live + box_rows - 1) / box_rows;
-            // lane = box: its page id is read while the slot is still in use
-            int page = 0;
-            if (lane < boxes) {
-                page = __ldg(pages + ((key0 + lane * box_rows) >> a.page_shift));
-                if (page < 0 || page >= a.n_pages) {
-                    raise_error(a.err, JANO_EINDEX);
-                    page = a.n_pages;                  // out of range: the copy fills zeros
-                }
-            }
-            const int s = i % L::kSlots;
-            if (!ctl.warp_wait(L::bEmpty + s, ((i / L::kSlots) & 1) ^ 1)) break;
+            const int shift = a.page_shift, page_rows = 1 << shift;
+            const int box_rows = min(page_rows, BN);
+            const int32_t* pages = a.table + (long long)seq * a.max_pages;
+            // the page ids of a load are read right after the load before it
+            // went out, so they arrive while its slot is still in use
+            int ids[kMaxBoxes];
+            auto read_ids = [&](int i) {
+                bool is_v;
+                const int key0 = (kt0 + order.tile(i, is_v)) * BN;
+                const int boxes = (min(seen - key0, BN) + box_rows - 1) / box_rows;
+#pragma unroll
+                for (int b = 0; b < kMaxBoxes; ++b)
+                    if (b < boxes) ids[b] = __ldg(pages + ((key0 + b * box_rows) >> shift));
+            };
+            read_ids(0);
+            int issued = 0;
+            for (int i = 0; i < 2 * n; ++i) {
+                bool is_v;
+                const int key0 = (kt0 + order.tile(i, is_v)) * BN;
+                const int live = min(seen - key0, BN);
+                const int boxes = (live + box_rows - 1) / box_rows;
+                const int s = i % L::kSlots;
+                if (!ctl.wait(L::bEmpty + s, ((i / L::kSlots) & 1) ^ 1)) break;
 #ifdef JANO_INJECT_DROP_LOAD
-            // failure-path test builds only: this tile is never issued, so the
-            // MMA's bounded wait for it runs out (JANO_ETIMEOUT)
-            if (i == JANO_INJECT_DROP_LOAD) continue;
+                // failure-path test builds only: this tile is never issued, so
+                // the MMA's bounded wait for it runs out (JANO_ETIMEOUT)
+                if (i == JANO_INJECT_DROP_LOAD) continue;
 #endif
-            const uint32_t bar = ctl.bar(is_v && live < BN ? L::bLast : L::bFull + s);
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box_rows * 128 * L::kPanels));
-            __syncwarp();
-            if (lane < boxes) {
-                const uint32_t dst = base + L::kRing + s * L::kTile + lane * box_rows * 128;
-                for (int p = 0; p < L::kPanels; ++p)
-                    tma_load_4d(dst + p * kPanel, is_v ? &tmV : &tmK, bar, p * 64, key0 & (page_rows - 1), head, page);
+                const uint32_t bar = ctl.bar(is_v && live < BN ? L::bLast : L::bFull + s);
+                ptx::mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box_rows * 128 * L::kPanels));
+                const CUtensorMap* tm = is_v ? &tmV : &tmK;
+                const uint32_t dst = base + L::kRing + s * L::kTile;
+#pragma unroll
+                for (int b = 0; b < kMaxBoxes; ++b)
+                    if (b < boxes) {
+                        int page = ids[b];
+                        if (page < 0 || page >= a.n_pages) {
+                            raise_error(a.err, JANO_EINDEX);
+                            page = a.n_pages;          // out of range: the copy fills zeros
+                        }
+                        for (int p = 0; p < L::kPanels; ++p)
+                            tma_load_4d(dst + b * box_rows * 128 + p * kPanel, tm, bar, p * 64,
+                                        key0 & (page_rows - 1), head, page);
+                    }
+                issued = i + 1;
+                if (issued < 2 * n) read_ids(issued);
             }
-            issued = i + 1;
-        }
-        // drain: every copy this CTA issued lands before its smem is released
-        if (lane == 0) {
+            // drain: every copy this CTA issued lands before its smem is released
             ptx::mbar_wait(ctl.bar(L::bQFull), 0, kWaitLimit);
             for (int i = max(0, issued - L::kSlots); i < issued; ++i) {
 #ifdef JANO_INJECT_DROP_LOAD
@@ -471,74 +600,88 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
       } else if (warp == 9 && n > 0) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc_qk = ptx::idesc_bf16(BM, BN, false, false);
             constexpr uint32_t idesc_pv = ptx::idesc_bf16(BM, HD, false, true);
             auto slot_of = [](int i) { return i % L::kSlots; };
-            auto wait_full = [&](int i) { return ctl.wait(L::bFull + slot_of(i), (i / L::kSlots) & 1, true); };
+            auto wait_full = [&](int i) { return ctl.poll(L::bFull + slot_of(i), (i / L::kSlots) & 1); };
             auto release = [&](int i) { ptx::mma_commit(ctl.bar(L::bEmpty + slot_of(i))); };
-            auto qk = [&](int st, int i) {         // S_st = Q K^T, K in load i's slot
-                const uint32_t kb = base + L::kRing + slot_of(i) * L::kTile;
-                const uint32_t qb = base + (st && !single ? L::kQ1 : 0u);
+            auto qk = [&](int st, uint32_t qb, int i) {    // S_st = Q K^T, K in load i's slot
+                const uint32_t kd = desc_lo(base + L::kRing + slot_of(i) * L::kTile, 16), qd = desc_lo(qb, 16);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * kPanel + (kk & 3) * 32;
-                    ptx::mma_ss(tmem + L::tS(st), ptx::smem_desc_sw128(qb + off, 16, 1024),
-                                ptx::smem_desc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+                    const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
+                    mma_ss(tmem + L::tS(st), qd + off, kd + off, idesc_qk, kk > 0);
                 }
                 ptx::mma_commit(ctl.bar(L::bSFull + st));
             };
             // O_st += P_st V over key sixteenths [k0, k1); V in load i's slot
             auto pv = [&](int st, int i, int k0, int k1, bool acc) {
-                const uint32_t vb = base + L::kRing + slot_of(i) * L::kTile;
+                const uint32_t vd = desc_lo(base + L::kRing + slot_of(i) * L::kTile, kPanel);
 #pragma unroll
                 for (int kk = k0; kk < k1; ++kk)
-                    ptx::mma_ts(tmem + L::tO(st), tmem + L::tS(st) + L::tP + kk * 8,
-                                ptx::smem_desc_sw128(vb + kk * 2048, kPanel, 1024), idesc_pv,
-                                (acc || kk > k0) ? 1u : 0u);
+                    mma_ts(tmem + L::tO(st), tmem + L::tS(st) + L::tP + kk * 8, vd + kk * 128, idesc_pv,
+                           acc || kk > k0);
             };
             auto pv_tile = [&](int st, int i, int j) -> bool {
-                if (!ctl.wait(L::bPHalf + st, j & 1, true)) return false;
+                if (!ctl.poll(L::bPHalf + st, j & 1)) return false;
                 ptx::tc_fence_after();
                 pv(st, i, BN / 32, BN / 16, j > 0);
-                if (!ctl.wait(L::bPFull + st, j & 1, true)) return false;
+                if (!ctl.poll(L::bPFull + st, j & 1)) return false;
                 ptx::tc_fence_after();
                 pv(st, i, 0, BN / 32, true);
                 return true;
             };
-            bool ok = ctl.wait(L::bQFull, 0);
+            bool ok = ctl.poll(L::bQFull, 0);
             if (!single) {
                 // S0_0 S1_0 | PV0_{j-1} S0_j PV1_{j-1} S1_j | ... PV0 PV1
-                for (int j = 0; ok && j <= n; ++j) {
-                    const int ik = order.k(j), iv = order.v(j - 1);
-                    if (j > 0 && !wait_full(iv)) { ok = false; break; }
-                    if (j < n && !wait_full(ik)) { ok = false; break; }
+                // (loads: K_j is 2j, V_j is 2j + 1)
+                if (ok && (ok = wait_full(0))) {
                     ptx::tc_fence_after();
-                    for (int st = 0; st < 2; ++st) {
-                        if (j > 0) {
-                            if (!pv_tile(st, iv, j - 1)) { ok = false; break; }
-                            if (j == n) ptx::mma_commit(ctl.bar(L::bOFull + st));
-                            if (st == 1) release(iv);
-                        }
-                        if (j < n) qk(st, ik);
+                    qk(0, base, 0);
+                    qk(1, base + L::kQ1, 0);
+                    release(0);
+                }
+                for (int j = 1; ok && j < n; ++j) {
+                    const int ik = 2 * j, iv = 2 * j - 1;
+                    if (!wait_full(iv) || !wait_full(ik)) { ok = false; break; }
+                    if (!pv_tile(0, iv, j - 1)) { ok = false; break; }
+                    qk(0, base, ik);
+                    if (!pv_tile(1, iv, j - 1)) { ok = false; break; }
+                    release(iv);
+                    qk(1, base + L::kQ1, ik);
+                    release(ik);
+                }
+                if (ok) {
+                    const int iv = 2 * n - 1;
+                    ok = wait_full(iv) && pv_tile(0, iv, n - 1);
+                    if (ok) {
+                        ptx::mma_commit(ctl.bar(L::bOFull + 0));
+                        ok = pv_tile(1, iv, n - 1);
                     }
-                    if (ok && j < n) release(ik);
+                    if (ok) {
+                        ptx::mma_commit(ctl.bar(L::bOFull + 1));
+                        release(iv);
+                    }
                 }
             } else {
                 // S0(0) S1(1) | PV(g) S(g+2) ... over the tiles g, stream g & 1
-                for (int g = -2; ok && g < n; ++g) {
-                    if (g >= 0) {
-                        if (!wait_full(order.v(g))) { ok = false; break; }
-                        ptx::tc_fence_after();
-                        if (!pv_tile(g & 1, order.v(g), g >> 1)) { ok = false; break; }
-                        release(order.v(g));
-                        if (g + 2 >= n) ptx::mma_commit(ctl.bar(L::bOFull + (g & 1)));
-                    }
-                    if (g + 2 < n) {
-                        if (!wait_full(order.k(g + 2))) { ok = false; break; }
-                        ptx::tc_fence_after();
-                        qk(g & 1, order.k(g + 2));
-                        release(order.k(g + 2));
+                const LoadOrder order{true, n};
+                for (int g = -2; ok && g < n; g += 2) {
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        const int v = g + st, k = g + st + 2;
+                        if (v >= 0 && v < n) {
+                            if (!wait_full(order.v(v)) || !pv_tile(st, order.v(v), v >> 1)) { ok = false; break; }
+                            release(order.v(v));
+                            if (k >= n) ptx::mma_commit(ctl.bar(L::bOFull + st));
+                        }
+                        if (k < n) {
+                            if (!wait_full(order.k(k))) { ok = false; break; }
+                            ptx::tc_fence_after();
+                            qk(st, base, order.k(k));
+                            release(order.k(k));
+                        }
                     }
                 }
             }
@@ -560,42 +703,71 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bFull + i % L::kSlots));
         }
       }
+      // the same barriers as the softmax warps' (both branches end for
+      // themselves: where they met again, the register counts would differ)
+      __syncwarp();
+      if (merge) {
+        if (n_split > 1) {
+            ptx::cluster_sync_all();
+            ptx::cluster_sync_all();
+        } else {
+            __syncthreads();
+        }
+      }
+      __syncthreads();
+      ptx::tc_fence_after();
+      if (warp == 9) ptx::tmem_dealloc(tmem, 512);
     } else {
         ptx::setmaxnreg_inc<kRegsSoftmax>();
         // ------------------------------------------------------------ softmax WG i
-        const int i = warp >> 2;
-        const int q = warp & 3;                       // TMEM lane quarter of this warp
+        const int i = uniform(warp >> 2);
+        const int q = uniform(warp & 3);              // TMEM lane quarter of this warp
         const int row = q * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q * 32) << 16;
         const uint32_t tS = tmem + lane_off + L::tS(i);
         const uint32_t tO = tmem + lane_off + L::tO(i);
-        const int rows = i && !single ? rows1 : rows0;         // query rows of this stream's tile
-        const int qrow = row0 + (i && !single ? a.tile_rows : 0) + row / a.group;
-        const bool live = row < rows * a.group;
-        const bool warp_live = q * 32 < rows * a.group;        // else only the barriers are kept
+        const bool warp_live = q * 32 < (i && !single ? rows1 : rows0) * a.group;   // else only the barriers are kept
         const int steps = single ? (n + 1 - i) >> 1 : n;
+        // the stream's tiles start at keys first, first + apart, ...
+        const int first = (kt0 + (single ? i : 0)) * BN, apart = single ? 2 * BN : BN;
         int limit = seen;
-        if (live && a.limits) limit = min(seen, __ldg(a.limits + qrow));
+        if (a.limits && row < (i && !single ? rows1 : rows0) * a.group)
+            limit = min(seen, __ldg(a.limits + row0 + (i && !single ? a.tile_rows : 0) + row / a.group));
+        // steps whose tile every row of the warp sees whole; the rest is masked
+        const int whole = __reduce_min_sync(0xFFFFFFFFu, limit) - first - BN;
+        const int plain = whole < 0 ? 0 : min(steps, whole / apart + 1);
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < steps; ++j) {
-            if (!ctl.warp_wait(L::bSFull + i, j & 1)) { ok = false; break; }
-            if (warp_live) {
+        int j = 0;
+        if (warp_live) {
+            for (; j < plain; ++j) {
+                if (!ctl.warp_wait(L::bSFull + i, j & 1)) break;
                 ptx::tc_fence_after();
-                const int valid = limit - (kt0 + (single ? 2 * j + i : j)) * BN;
-                if (__any_sync(0xFFFFFFFFu, valid < BN))
-                    softmax_tile<HD, true>(tS, tO, tS + L::tP, j == 0, valid, a.scale_log2, m, l,
-                                           ctl.bar(L::bPHalf + i));
-                else
-                    softmax_tile<HD, false>(tS, tO, tS + L::tP, j == 0, BN, a.scale_log2, m, l,
-                                            ctl.bar(L::bPHalf + i));
+                softmax_tile<HD, false>(tS, BN, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
                 ptx::tc_fence_before();
                 __syncwarp();
-            } else if (lane == 0) {
-                ptx::mbar_arrive(ctl.bar(L::bPHalf + i));
+                if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + i));
             }
-            if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + i));
+            for (; j < steps; ++j) {
+                if (!ctl.warp_wait(L::bSFull + i, j & 1)) break;
+                ptx::tc_fence_after();
+                softmax_tile<HD, true>(tS, limit - first - j * apart, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + i));
+            }
+        } else {
+            for (; j < steps; ++j) {
+                if (!ctl.warp_wait(L::bSFull + i, j & 1)) break;
+                if (lane == 0) {
+                    ptx::mbar_arrive(ctl.bar(L::bPHalf + i));
+                    ptx::mbar_arrive(ctl.bar(L::bPFull + i));
+                }
+            }
         }
+        const bool ok = j == steps;
+        const int tile = i && !single ? 1 : 0;
+        const int qrow = row0 + tile * a.tile_rows + row / a.group;
+        const bool live = row < (tile ? rows1 : rows0) * a.group;
         // ------------------------------------------------------------ epilogue
         // before a merge every MMA of the CTA is done: O goes where they read
         bool done = ok;
@@ -645,75 +817,19 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 }
             }
         }
-    }
-
-    if (merge) {
-        // Parts of a tile row: one per CTA of the cluster, two (the streams)
-        // in the single form.  With M the largest m and w = 2^(m - M),
-        //   out = sum w O / sum w l,   summed in a fixed order.
-        __syncwarp();
-        if (n_split > 1) ptx::cluster_sync_all();
-        else __syncthreads();
-        constexpr int E = HD / 32;                     // columns per lane
-        const int packed0 = rows0 * a.group, total = packed0 + rows1 * a.group;
-        const int parts = single ? 2 * n_split : n_split;
-        for (int r = split * (kThreads / 32) + warp; r < total; r += n_split * (kThreads / 32)) {
-            const int tile = r >= packed0, p = tile ? r - packed0 : r;
-            // lane = part: its address, weight and share of the sum
-            const int z = single ? lane >> 1 : lane, st = single ? lane & 1 : tile;
-            uint32_t row_addr = 0;
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (lane < parts) {
-                const uint32_t peer = ptx::mapa_shared(base, (uint32_t)z);
-                ml = ld_cluster_f2(peer + L::kMl + (st * BM + p) * 8);
-                row_addr = peer + (st * BM + p) * L::kRow * 4;
-            }
-            if (__any_sync(0xFFFFFFFFu, ml.y < 0.f)) continue;     // a part is missing: JANO_ETIMEOUT was raised
-            float M = ml.x, sum;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-            // a part without visible keys has m = -inf, l = 0 and no O
-            const float w = ml.y != 0.f ? ptx::ex2(ml.x - M) : 0.f;
-            sum = w * ml.y;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            float acc[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = 0.f;
-            for (int c = 0; c < parts; ++c) {
-                const float wc = __shfl_sync(0xFFFFFFFFu, w, c);
-                const uint32_t ac = __shfl_sync(0xFFFFFFFFu, row_addr, c);
-                if (wc != 0.f) {
-                    if constexpr (E == 4) {
-                        const float4 o = ld_cluster_f4(ac + lane * 16);
-                        acc[0] = fmaf(wc, o.x, acc[0]);
-                        acc[1] = fmaf(wc, o.y, acc[1]);
-                        acc[2] = fmaf(wc, o.z, acc[2]);
-                        acc[3] = fmaf(wc, o.w, acc[3]);
-                    } else {
-                        const float2 o = ld_cluster_f2(ac + lane * 8);
-                        acc[0] = fmaf(wc, o.x, acc[0]);
-                        acc[1] = fmaf(wc, o.y, acc[1]);
-                    }
-                }
-            }
-            const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-            __nv_bfloat16* dst = a.out + (long long)(row0 + tile * a.tile_rows + p / a.group) * a.out_ld +
-                                 (head * a.group + p % a.group) * HD + lane * E;
-            if constexpr (E == 4)
-                *reinterpret_cast<uint2*>(dst) =
-                    make_uint2(ptx::pack_bf16(acc[0] * inv, acc[1] * inv), ptx::pack_bf16(acc[2] * inv, acc[3] * inv));
-            else
-                *reinterpret_cast<uint32_t*>(dst) = ptx::pack_bf16(acc[0] * inv, acc[1] * inv);
+        // ------------------------------------------------------------ merge
+        if (merge) {
+            __syncwarp();
+            if (n_split > 1) ptx::cluster_sync_all();
+            else __syncthreads();
+            merge_rows<HD>(a);
+            // no CTA leaves while a peer may still read its shared memory
+            __syncwarp();
+            if (n_split > 1) ptx::cluster_sync_all();
         }
-        // no CTA leaves while a peer may still read its shared memory
-        __syncwarp();
-        if (n_split > 1) ptx::cluster_sync_all();
+        ptx::tc_fence_before();
+        __syncthreads();
     }
-    ptx::tc_fence_before();
-    __syncthreads();
-    ptx::tc_fence_after();
-    if (warp == 9) ptx::tmem_dealloc(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -813,9 +929,14 @@ cudaError_t launch_hd(const PagedAttentionCall& c, const Args& a, int tiles, int
     if (!make_q_map(&mq, c.q, c.q_ld, c.n_rows, c.heads, HD, a.group, a.tile_rows) ||
         !make_pool_map(&mk, c.pool->k, *c.pool) || !make_pool_map(&mv, c.pool->v, *c.pool))
         return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)tiles, (unsigned)c.pool->kv_heads, (unsigned)split);
+    if (split == 1) {
+        paged_attention_kernel<HD><<<grid, kThreads, L::kAlloc, st>>>(mq, mk, mv, a);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)tiles, (unsigned)c.pool->kv_heads, (unsigned)split);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = L::kAlloc;
     cfg.stream = st;
