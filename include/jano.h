@@ -578,19 +578,30 @@ JANO_API jano_status jano_paged_append(const jano_page_pool *pool, const jano_pa
  * max_rows, max_len  upper bounds of a sequence's rows and length (grid and
  *          split choice only); a sequence above either, or with a bad length
  *          or cu_rows, raises JANO_EINDEX and its rows are not written.
- * n_split  CTAs that share one query tile's keys: 1, 2, 4, 8 or 16 (a
- *          thread-block cluster; 16 falls to 8 where the device cannot run
- *          such clusters), or 0 for the library's choice.
+ * n_split  CTAs that share one query tile's keys: 1, 2, 4 or 8 (a
+ *          thread-block cluster), or 0 for the library's choice.
  * A page id outside the pool raises JANO_EINDEX and reads as zeros.  K and V
  * at positions below the sequence's length must be finite; places past it
  * may hold anything.  BF16 in, fp32 accumulation and softmax, BF16 out.
- * Deterministic.  No workspace.
+ * workspace  device scratch of ws_bytes >= jano_paged_attention_workspace_bytes
+ *          bytes, 16-byte aligned, or NULL.  With n_split = 0 and few rows per
+ *          sequence (the query's bytes are not 0) it selects the form for
+ *          them: every SM takes an equal share of all key tiles, whatever the
+ *          lengths, and the partials at the shares' ends go through it.  Its
+ *          contents are overwritten and need no zeroing; calls that may
+ *          overlap need workspaces of their own.
+ * Deterministic.
  * ---------------------------------------------------------------------- */
 JANO_API jano_status jano_paged_attention(const jano_page_pool *pool, const jano_page_seqs *seqs,
                                           const void *q, long long q_ld, const int32_t *limits,
                                           int n_rows, int max_rows, int max_len, int heads,
-                                          float scale, int n_split, void *out, long long out_ld,
-                                          void *stream);
+                                          float scale, int n_split, void *workspace, size_t ws_bytes,
+                                          void *out, long long out_ld, void *stream);
+
+/* Workspace bytes of a call on the current device: 2 SMs * max_rows * (heads
+ * / kv_heads) rows of d + 2 floats where that product of rows is at most 32,
+ * else 0 (also on invalid arguments). */
+JANO_API size_t jano_paged_attention_workspace_bytes(int max_rows, int heads, int kv_heads, int d);
 
 /* The split jano_paged_attention takes for n_split = 0 on a device of
  * sm_count SMs (host only); 1 on invalid arguments. */

@@ -15,7 +15,6 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-import struct
 from dataclasses import dataclass
 
 import torch
@@ -30,7 +29,7 @@ __all__ = [
     "kv_scatter", "active_attention", "device_error",
     "jano_rope_cfg", "jano_page_pool", "jano_page_seqs", "jano_rope_table_floats", "jano_rope_table",
     "jano_axis_rope", "jano_rope_scatter", "jano_paged_append", "jano_paged_attention",
-    "jano_paged_attention_splits_on", "Rope", "rope_table", "axis_rope", "rope_scatter", "page_pool",
+    "jano_paged_attention_workspace_bytes", "jano_paged_attention_splits_on", "Rope", "rope_table", "axis_rope", "rope_scatter", "page_pool",
     "paged_append", "paged_attention",
 ]
 
@@ -47,8 +46,8 @@ EXPORTS = ("jano_block_scores", "jano_block_scores_literal", "jano_classify", "j
            "jano_active_attention_split", "jano_active_attention_workspace_bytes", "jano_active_attention_splits",
            "jano_active_attention_splits_on", "jano_gather_gemm", "jano_qkv_project", "jano_random_scores", "jano_fft_scores",
            "jano_stream_sum", "jano_rope_table_floats", "jano_rope_table", "jano_axis_rope", "jano_rope_scatter",
-           "jano_paged_append", "jano_paged_attention", "jano_paged_attention_splits_on",
-           "jano_get_device_error", "jano_status_str", "jano_version")
+           "jano_paged_append", "jano_paged_attention", "jano_paged_attention_workspace_bytes",
+           "jano_paged_attention_splits_on", "jano_get_device_error", "jano_status_str", "jano_version")
 
 
 class JanoError(RuntimeError):
@@ -115,15 +114,17 @@ def lib() -> C.CDLL:
         L.jano_random_scores.argtypes = [i, C.c_uint64, P, P]
         L.jano_fft_scores.argtypes = [P, i, G, i, P, P]
         L.jano_stream_sum.argtypes = [P, C.c_longlong, P, i, P]
-        ll, R = C.c_longlong, C.POINTER(jano_rope_cfg)
-        pool, seqs = C.POINTER(jano_page_pool), C.POINTER(jano_page_seqs)
+        # structure pointers as void: they take ctypes objects by reference and packed bytes
+        ll, R, pool, seqs = C.c_longlong, P, P, P
         L.jano_rope_table_floats.argtypes = [R]
         L.jano_rope_table_floats.restype = z
         L.jano_rope_table.argtypes = [R, C.c_double, i, P, P]
         L.jano_axis_rope.argtypes = [P, ll, P, P, i, i, i, R, P, P, ll, P]
         L.jano_rope_scatter.argtypes = [P, ll, P, ll, P, ll, P, P, i, i, i, i, R, P, P, ll, P, P, i, P]
         L.jano_paged_append.argtypes = [pool, seqs, P, ll, P, ll, P, ll, P, P, P, i, i, R, P, P, ll, P]
-        L.jano_paged_attention.argtypes = [pool, seqs, P, ll, P, i, i, i, i, f, i, P, ll, P]
+        L.jano_paged_attention.argtypes = [pool, seqs, P, ll, P, i, i, i, i, f, i, P, z, P, ll, P]
+        L.jano_paged_attention_workspace_bytes.argtypes = [i, i, i, i]
+        L.jano_paged_attention_workspace_bytes.restype = z
         L.jano_paged_attention_splits_on.argtypes = [i, i, i, i, i, i, i]
         L.jano_get_device_error.argtypes = [P]
         L.jano_status_str.argtypes = [i]
@@ -169,60 +170,6 @@ def _dev(t: torch.Tensor | None, name: str, dtype=None) -> int | None:
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
-
-
-def _addr(t: torch.Tensor | None) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
-def _here(**tensors) -> None:
-    """Every given tensor lies on the current CUDA device (the kernels are
-    launched there)."""
-    cur = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        dev = t.get_device()                 # -1 on the CPU
-        if dev == cur:
-            continue
-        if dev < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if dev != cur:
-            raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{cur}")
-
-
-def _rows(t: torch.Tensor, name: str, heads: int | None = None, d: int | None = None) -> int:
-    """Row distance of a BF16 tensor [rows][heads][d] whose heads and columns
-    are adjacent (rows may be slices of a wider buffer)."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows][heads][d], got {tuple(t.shape)}")
-    n, h, c = t.shape
-    if (heads is not None and h != heads) or (d is not None and c != d):
-        raise ValueError(f"{name} must be [rows][{heads}][{d}], got {tuple(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if (c > 1 and s2 != 1) or (h > 1 and s1 != c):
-        raise ValueError(f"the heads and columns of {name}'s rows must be adjacent")
-    if n <= 1:
-        return h * c if h * c % 8 == 0 else -(-h * c // 8) * 8
-    return s0
-
-
-def _count(t: torch.Tensor | None, name: str, n: int) -> None:
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
-
-
-def _on_stream(stream, shape, like: torch.Tensor) -> torch.Tensor:
-    """A new tensor for a launch on `stream` (allocated there, so the memory's
-    earlier uses are ordered before it)."""
-    if stream is None:
-        return like.new_empty(shape)
-    with torch.cuda.stream(_torch_stream(stream)):
-        return like.new_empty(shape)
 
 
 def _check(fn: str, code: int) -> None:
@@ -364,36 +311,35 @@ def jano_rope_table(cfg, theta, shared_freq, table, stream=None):
         C.byref(cfg), theta, shared_freq, _dev(table, "table", torch.float32), _stream(stream)))
 
 
-def jano_axis_rope(x, x_ld, ids, coords, n_rows, heads, d, cfg, table, out, out_ld, stream=None):
-    """x and out as (device address, row distance) or tensors whose rows lie x_ld / out_ld elements apart."""
-    _check("jano_axis_rope", lib().jano_axis_rope(
-        _addr(x), x_ld, _dev(ids, "ids", torch.int32), _dev(coords, "coords", torch.int32), n_rows, heads, d,
-        C.byref(cfg), _dev(table, "table", torch.float32), _addr(out), out_ld, _stream(stream)))
+# In the four calls below row buffers (x, q, k, v, out) are device addresses with their row distances, and the
+# structures ctypes objects or their packed bytes: paged.py makes both from tensors.
+def jano_axis_rope(x, x_ld, ids, coords, n_rows, heads, d, cfg, table, out, out_ld, stream):
+    _check("jano_axis_rope", lib().jano_axis_rope(x, x_ld, ids, coords, n_rows, heads, d, cfg, table, out, out_ld,
+                                                  stream))
 
 
 def jano_rope_scatter(q, q_ld, k, k_ld, v, v_ld, idx, coords, n_act, heads, kv_heads, d, cfg, table, q_out, q_out_ld,
-                      k_cache, v_cache, n_tokens, stream=None):
-    _check("jano_rope_scatter", lib().jano_rope_scatter(
-        _addr(q), q_ld, _addr(k), k_ld, _addr(v), v_ld, _dev(idx, "idx", torch.int32),
-        _dev(coords, "coords", torch.int32), n_act, heads, kv_heads, d, C.byref(cfg),
-        _dev(table, "table", torch.float32), _addr(q_out), q_out_ld, _dev(k_cache, "k_cache", torch.bfloat16),
-        _dev(v_cache, "v_cache", torch.bfloat16), n_tokens, _stream(stream)))
+                      k_cache, v_cache, n_tokens, stream):
+    _check("jano_rope_scatter", lib().jano_rope_scatter(q, q_ld, k, k_ld, v, v_ld, idx, coords, n_act, heads, kv_heads,
+                                                        d, cfg, table, q_out, q_out_ld, k_cache, v_cache, n_tokens,
+                                                        stream))
 
 
 def jano_paged_append(pool, seqs, q, q_ld, k, k_ld, v, v_ld, pos, coords, grids, n_rows, heads, cfg, table, q_out,
-                      q_out_ld, stream=None):
-    _check("jano_paged_append", lib().jano_paged_append(
-        C.byref(pool), C.byref(seqs), _addr(q), q_ld, _addr(k), k_ld, _addr(v), v_ld, _dev(pos, "pos", torch.int32),
-        _dev(coords, "coords", torch.int32), _dev(grids, "grids", torch.int32), n_rows, heads,
-        None if cfg is None else C.byref(cfg), _dev(table, "table", torch.float32), _addr(q_out), q_out_ld,
-        _stream(stream)))
+                      q_out_ld, stream):
+    _check("jano_paged_append", lib().jano_paged_append(pool, seqs, q, q_ld, k, k_ld, v, v_ld, pos, coords, grids,
+                                                        n_rows, heads, cfg, table, q_out, q_out_ld, stream))
 
 
-def jano_paged_attention(pool, seqs, q, q_ld, limits, n_rows, max_rows, max_len, heads, scale, n_split, out, out_ld,
-                         stream=None):
-    _check("jano_paged_attention", lib().jano_paged_attention(
-        C.byref(pool), C.byref(seqs), _addr(q), q_ld, _dev(limits, "limits", torch.int32), n_rows, max_rows, max_len,
-        heads, scale, n_split, _addr(out), out_ld, _stream(stream)))
+def jano_paged_attention(pool, seqs, q, q_ld, limits, n_rows, max_rows, max_len, heads, scale, n_split, workspace,
+                         ws_bytes, out, out_ld, stream):
+    _check("jano_paged_attention", lib().jano_paged_attention(pool, seqs, q, q_ld, limits, n_rows, max_rows, max_len,
+                                                              heads, scale, n_split, workspace, ws_bytes, out, out_ld,
+                                                              stream))
+
+
+def jano_paged_attention_workspace_bytes(max_rows, heads, kv_heads, d) -> int:
+    return int(lib().jano_paged_attention_workspace_bytes(max_rows, heads, kv_heads, d))
 
 
 def jano_paged_attention_splits_on(n_rows, max_rows, max_len, n_seqs, heads, kv_heads, sm_count) -> int:
@@ -604,209 +550,5 @@ def device_error(stream=None) -> int:
     return jano_get_device_error(stream)
 
 
-# ---------------------------------------------------------------- rotary positions and the paged cache
-@dataclass(frozen=True)
-class Rope:
-    """Rotary positions with up to three axes (frame, row, column).
-
-    axes    columns of a head that each axis turns (even; their sum at most d);
-    n_pos   positions per axis that the table holds;
-    grid    (rows, columns) of the token grid, for token ids without explicit
-            coordinates;
-    pairing "interleaved": columns (2s, 2s + 1); "halves": (s, s + rot / 2);
-    shared  one frequency series over all slots instead of one per axis."""
-    axes: tuple
-    n_pos: tuple
-    grid: tuple = (0, 0)
-    theta: float = 10000.0
-    pairing: str = "interleaved"
-    shared: bool = False
-
-    def __post_init__(self):
-        if self.pairing not in ("interleaved", "halves"):
-            raise ValueError(f"pairing must be 'interleaved' or 'halves', got {self.pairing!r}")
-        if len(self.axes) != 3 or len(self.n_pos) != 3 or len(self.grid) != 2:
-            raise ValueError("axes and n_pos have three entries, grid has two")
-
-    @classmethod
-    def of(cls, geom: "Geometry", axes, **kw) -> "Rope":
-        """The rotation over a geometry's token grid."""
-        pf, ph, pw = geom.patch
-        n = (geom.F // pf, geom.H // ph, geom.W // pw)
-        return cls(axes=tuple(axes), n_pos=n, grid=n[1:], **kw)
-
-    def c(self) -> jano_rope_cfg:
-        return jano_rope_cfg.from_buffer_copy(_ROPE(*self.axes, *self.n_pos, *self.grid, self.pairing == "halves"))
-
-    @property
-    def table_shape(self) -> tuple:
-        return (sum(n * (a // 2) for a, n in zip(self.axes, self.n_pos)), 2)
-
-
-def _table(rope: Rope, table: torch.Tensor) -> None:
-    (a, b, c), (x, y, z) = rope.axes, rope.n_pos
-    _count(table, "table", 2 * (x * (a // 2) + y * (b // 2) + z * (c // 2)))
-
-
-def rope_table(rope: Rope, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """The (cos, sin) table of a rotation, fp32 [entries][2]: axis 0's
-    positions x slots, then axis 1's, then axis 2's."""
-    if out is None:
-        dev = torch.empty(0, dtype=torch.float32, device="cuda")
-        out = _on_stream(stream, rope.table_shape, dev)
-    _here(out=out)
-    _table(rope, out)
-    jano_rope_table(rope.c(), rope.theta, int(rope.shared), out, stream)
-    return out
-
-
-def axis_rope(x, rope: Rope, table, ids=None, coords=None, out=None, stream=None) -> torch.Tensor:
-    """x [rows][heads][d] rotated by each row's position: of token ids[r]
-    (default r) on the rope's grid, or at coords [rows][3].  out may be x."""
-    ld = _rows(x, "x")
-    n, h, d = x.shape
-    _here(x=x, table=table, ids=ids, coords=coords, out=out)
-    _table(rope, table)
-    _count(ids, "ids", n)
-    _count(coords, "coords", 3 * n)
-    if out is None:
-        out = _on_stream(stream, (n, h, d), x)
-    elif out.shape[0] != n:
-        raise ValueError(f"out must have {n} rows, got {out.shape[0]}")
-    jano_axis_rope(x, ld, ids, coords, n, h, d, rope.c(), table, out, _rows(out, "out", h, d), stream)
-    return out
-
-
-def _queries(q, q_out, n, d, stream):
-    """(q, its row distance, q_out, its row distance, heads) of an append; q may be None."""
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        return None, 0, None, 0, 1
-    ld = _rows(q, "q", None, d)
-    if q.shape[0] != n:
-        raise ValueError(f"q must have {n} rows, got {q.shape[0]}")
-    h = q.shape[1]
-    if q_out is None:
-        q_out = _on_stream(stream, (n, h, d), q)
-    elif q_out.shape[0] != n:
-        raise ValueError(f"q_out must have {n} rows, got {q_out.shape[0]}")
-    return q, ld, q_out, _rows(q_out, "q_out", h, d), h
-
-
-def rope_scatter(k, v, idx, k_cache, v_cache, rope: Rope, table, q=None, q_out=None, coords=None, stream=None):
-    """kv_scatter with the rotation on the way: rows idx of the caches
-    [N][kv_heads][d] become the rotated k and v; the queries q [n][heads][d]
-    are rotated in the same launch (into q_out, which may be q; returned)."""
-    n = idx.numel()
-    N, h, d = k_cache.shape
-    _here(k=k, v=v, idx=idx, k_cache=k_cache, v_cache=v_cache, table=table, q=q, q_out=q_out, coords=coords)
-    k_ld, v_ld = _rows(k, "k", h, d), _rows(v, "v", h, d)
-    if k.shape[0] != n or v.shape[0] != n or v_cache.shape != k_cache.shape:
-        raise ValueError("k, v and idx must have as many rows, and both caches one shape")
-    _table(rope, table)
-    _count(coords, "coords", 3 * n)
-    q, q_ld, q_out, o_ld, heads = _queries(q, q_out, n, d, stream)
-    jano_rope_scatter(q, q_ld, k, k_ld, v, v_ld, idx, coords, n, heads, h, d, rope.c(), table, q_out, o_ld,
-                      k_cache, v_cache, N, stream)
-    return q_out
-
-
-def page_pool(n_pages: int, page_size: int, kv_heads: int, d: int, head_major: bool = False, device="cuda"):
-    """Empty K and V pages, each [n_pages][page_size][kv_heads][d] (head_major:
-    a head's places are adjacent in memory)."""
-    shape = (n_pages, kv_heads, page_size, d) if head_major else (n_pages, page_size, kv_heads, d)
-    k, v = (torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
-    return (k.transpose(1, 2), v.transpose(1, 2)) if head_major else (k, v)
-
-
-# the C structures packed in one step (a third of the time of their constructors)
-_ROPE = struct.Struct("9i").pack
-_POOL = struct.Struct("PP4i3q").pack
-_SEQS = struct.Struct("PPP2i").pack
-
-
-def _pool(k_pages, v_pages) -> jano_page_pool:
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [pages][page_size][kv_heads][d], got {tuple(t.shape)}")
-    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
-        raise ValueError("k_pages and v_pages must have one shape and the same strides")
-    n, p, h, d = k_pages.shape
-    s0, s1, s2, s3 = k_pages.stride()
-    if d > 1 and s3 != 1:
-        raise ValueError("the columns of a head must be adjacent")
-    # the stride of a dimension of one element is any number: one that passes the checks
-    return jano_page_pool.from_buffer_copy(_POOL(k_pages.data_ptr(), v_pages.data_ptr(), n, p, h, d,
-                                                 s0 if n > 1 else p * h * d, s1, s2 if h > 1 else d))
-
-
-def _seqs(page_table, seq_lens, cu_rows) -> jano_page_seqs:
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table must be [sequences][pages], got {tuple(page_table.shape)}")
-    n = page_table.shape[0]
-    _count(seq_lens, "seq_lens", n)
-    _count(cu_rows, "cu_rows", n + 1)
-    return jano_page_seqs.from_buffer_copy(_SEQS(
-        _dev(page_table, "page_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
-        _dev(cu_rows, "cu_rows", torch.int32), n, page_table.shape[1]))
-
-
-def paged_append(k, v, pos, k_pages, v_pages, page_table, seq_lens, cu_rows, rope: Rope | None = None, table=None,
-                 q=None, q_out=None, coords=None, grids=None, stream=None):
-    """Write new K/V rows [n][kv_heads][d] at positions pos of their sequences
-    (sequence s owns rows cu_rows[s]:cu_rows[s+1]; seq_lens counts them in),
-    K rotated on the way when a rope and its table are given, and the queries
-    q [n][heads][d] with it (into q_out, which may be q; returned).  A row's
-    coordinates come from coords [n][3], or from pos on its sequence's grid
-    (grids [sequences][2], or the rope's)."""
-    n = pos.numel()
-    h, d = k_pages.shape[-2:]
-    _here(k=k, v=v, pos=pos, k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
-          cu_rows=cu_rows, table=table, q=q, q_out=q_out, coords=coords, grids=grids)
-    k_ld, v_ld = _rows(k, "k", h, d), _rows(v, "v", h, d)
-    if k.shape[0] != n or v.shape[0] != n:
-        raise ValueError("k, v and pos must have as many rows")
-    if rope is None and (table is not None or coords is not None or grids is not None):
-        raise ValueError("table, coords and grids need a rope")
-    if rope is not None:
-        if table is None:
-            raise ValueError("a rope needs its table")
-        _table(rope, table)
-    _count(coords, "coords", 3 * n)
-    _count(grids, "grids", 2 * page_table.shape[0])
-    q, q_ld, q_out, o_ld, heads = _queries(q, q_out, n, d, stream)
-    jano_paged_append(_pool(k_pages, v_pages), _seqs(page_table, seq_lens, cu_rows), q, q_ld, k, k_ld, v, v_ld, pos,
-                      coords, grids, n, heads, None if rope is None else rope.c(), table, q_out, o_ld, stream)
-    return q_out
-
-
-def paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_rows, out=None, limits=None, max_rows=None,
-                    max_len=None, scale=None, split=0, stream=None) -> torch.Tensor:
-    """Attention of the rows q [n][heads][d] of several sequences over their
-    pages; row r sees the first min(seq_lens[s], limits[r]) positions (all of
-    them without limits; none: zeros).  max_rows / max_len: upper bounds of a
-    sequence's rows and length, if known (they size the grid and choose the
-    split); split: CTAs that share one query tile's keys (0: the library's
-    choice).  Rows past cu_rows[-1] of out are left as they are."""
-    q_ld = _rows(q, "q")
-    n, h, d = q.shape
-    _here(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens, cu_rows=cu_rows, out=out,
-          limits=limits)
-    if k_pages.shape[-1] != d:
-        raise ValueError(f"q and the pages must have one head size, got {d} and {k_pages.shape[-1]}")
-    _count(limits, "limits", n)
-    if out is None:
-        out = _on_stream(stream, (n, h, d), q)
-    elif out.shape[0] != n:
-        raise ValueError(f"out must have {n} rows, got {out.shape[0]}")
-    if max_rows is None:
-        max_rows = n
-    if max_len is None:
-        max_len = page_table.shape[1] * k_pages.shape[1]
-    jano_paged_attention(_pool(k_pages, v_pages), _seqs(page_table, seq_lens, cu_rows), q, q_ld, limits, n, max_rows,
-                         max_len, h, d ** -0.5 if scale is None else scale, split, out, _rows(out, "out", h, d),
-                         stream)
-    return out
+from .paged import (Rope, axis_rope, page_pool, paged_append, paged_attention, rope_scatter,  # noqa: E402
+                    rope_table)

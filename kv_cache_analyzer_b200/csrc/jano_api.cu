@@ -322,6 +322,12 @@ jano_status check_qkv(const RopeCacheCall& r) {
     return check_rows(r.v, r.v_ld, k_w);
 }
 
+int current_sms() {
+    int dev = 0, sms = 0;
+    return cudaGetDevice(&dev) == cudaSuccess &&
+                   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? sms : 0;
+}
+
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 }  // namespace
 
@@ -401,10 +407,11 @@ jano_status jano_paged_append(const jano_page_pool* pool, const jano_page_seqs* 
 
 jano_status jano_paged_attention(const jano_page_pool* pool, const jano_page_seqs* seqs, const void* q, long long q_ld,
                                  const int32_t* limits, int n_rows, int max_rows, int max_len, int heads,
-                                 float scale, int n_split, void* out, long long out_ld, void* stream) {
+                                 float scale, int n_split, void* workspace, size_t ws_bytes, void* out,
+                                 long long out_ld, void* stream) {
     if (n_rows < 0 || max_rows < 0 || max_len < 0 || heads < 1) return JANO_EINVAL;
     if (!(scale > 0.0f) || !std::isfinite(scale)) return JANO_EINVAL;
-    if (n_split < 0 || n_split > 16 || (n_split & (n_split - 1))) return JANO_EINVAL;
+    if (n_split < 0 || n_split > 8 || (n_split & (n_split - 1))) return JANO_EINVAL;
     if (n_rows == 0) return JANO_OK;
     jano_status s = check_pool(pool, seqs);
     if (s != JANO_OK) return s;
@@ -414,11 +421,26 @@ jano_status jano_paged_attention(const jano_page_pool* pool, const jano_page_seq
     if (q_ld >= (1ll << 38) || (long long)heads * pool->d > INT_MAX) return JANO_EUNSUPPORTED;
     if ((s = check_rows(q, q_ld, (long long)heads * pool->d)) != JANO_OK) return s;
     if ((s = check_rows(out, out_ld, (long long)heads * pool->d)) != JANO_OK) return s;
+    if (!aligned16(workspace)) return JANO_EALIGN;
     int* err = device_error_word();
     if (!err) return JANO_ECUDA;
     const PagedAttentionCall c{pool, seqs, q, q_ld, limits, n_rows, max_rows < 1 ? 1 : max_rows, max_len, heads,
-                               scale, n_split, out, out_ld};
+                               scale, n_split, workspace, out, out_ld};
+    if (n_split == 0 && workspace) {
+        const int sms = current_sms();
+        if (sms < 1) return JANO_ECUDA;
+        const size_t need = paged_decode_workspace_bytes(c.max_rows, heads, pool->kv_heads, pool->d, sms);
+        if (ws_bytes < need) return JANO_EINVAL;
+        if (need > 0 && paged_decode_fits(c))
+            return from_cuda(launch_paged_decode(c, sms, err, static_cast<cudaStream_t>(stream)));
+    }
     return from_cuda(launch_paged_attention(c, err, static_cast<cudaStream_t>(stream)));
+}
+
+size_t jano_paged_attention_workspace_bytes(int max_rows, int heads, int kv_heads, int d) {
+    if (max_rows < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || (d != 64 && d != 128)) return 0;
+    const int sms = current_sms();
+    return sms < 1 ? 0 : paged_decode_workspace_bytes(max_rows, heads, kv_heads, d, sms);
 }
 
 int jano_paged_attention_splits_on(int n_rows, int max_rows, int max_len, int n_seqs, int heads, int kv_heads,

@@ -120,10 +120,15 @@ struct PagedAttentionCall {
     int n_rows, max_rows, max_len, heads;
     float scale;
     int n_split;                             // CTAs per (query tiles, K/V head); 0: paged_split_count
+    void* workspace;                         // few rows per sequence: partials of launch_paged_decode
     void* out;
     long long out_ld;
 };
 cudaError_t launch_paged_attention(const PagedAttentionCall& c, int* err, cudaStream_t st);
+// Few rows per sequence (a workspace of more than 0 bytes says it applies).
+bool paged_decode_fits(const PagedAttentionCall& c);
+cudaError_t launch_paged_decode(const PagedAttentionCall& c, int sms, int* err, cudaStream_t st);
+size_t paged_decode_workspace_bytes(int max_rows, int heads, int kv_heads, int d, int sms);
 int paged_split_count(int n_rows, int max_rows, int max_len, int n_seqs, int heads, int kv_heads, int sms);
 
 cudaError_t launch_random_scores(int n, uint64_t seed, float* scores, cudaStream_t st);

@@ -23,15 +23,16 @@
 // Which one a CTA takes is decided by its own sequence's rows, so one launch
 // serves single tokens and long chunks together.
 //
-// Few rows leave SMs idle: the key tiles are then cut over the 2 to 16 CTAs
+// Few rows leave SMs idle: the key tiles are then cut over the 2 to 8 CTAs
 // of a thread-block cluster, which merge their (O, m, l) through distributed
 // shared memory -- no workspace, no second launch, and a fixed order of sums.
 //
 // 12 warps: 0-3 and 4-7 softmax warpgroups (thread = tile row = TMEM lane),
-// 8 TMA producer, 9 MMA issuer, 10 clears V rows past the visible length
-// (stale pages may hold NaN there, and 0 * NaN would reach O), 11 idle.  A
+// 8 producer of Q and K, 9 MMA issuer, 10 clears V rows past the visible
+// length (stale pages may hold NaN there, and 0 * NaN would reach O), 11
+// producer of V.  A
 // 128-key tile is gathered page by page: one box of min(page_size, 128) rows
-// x 64 columns per page and panel.  The producer and the MMA issuer each run as
+// x 64 columns per page and panel.  The producers and the MMA issuer each run as
 // one elected thread: elect.sync lets the compiler keep their operands in
 // uniform registers, which halved the MMA thread's time per key tile.
 // The pool's map has page, head and token strides of its own, so token-major
@@ -44,20 +45,13 @@
 // grows by more than 2^8, which keeps P within BF16's range either way.
 // Every wait is bounded; a CTA that gives up records JANO_ETIMEOUT, takes
 // part in the cluster's barriers, and the rows it shares are not written.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cudaTypedefs.h>
-
 #include <cmath>
-#include <mutex>
 
-#include "jano_common.cuh"
+#include "paged_tile.cuh"
 
 namespace jano {
 namespace {
 
-constexpr int BM = 128;            // tile rows
-constexpr int BN = 128;            // keys per tile
 constexpr int kThreads = 384;
 // As launched 384 x 168 registers; the softmax warpgroups hold a whole
 // 128-column S row per thread.  2 x 128 x 208 + 128 x 80 <= 384 x 168.
@@ -66,29 +60,29 @@ constexpr int kRegsSoftmax = 208;
 constexpr int kRegsIssue = 80;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
 static_assert(2 * kRegsSoftmax + kRegsIssue <= 512, "sub-partition register file");
-constexpr uint32_t kPanel = 128 * 128;       // bytes of one 128-row x 64-column panel
 constexpr int kSoftmaxWarps = 8;
-constexpr int kMaxSplit = 16;
-constexpr int kMaxBoxes = 8;         // pages of 16 rows in a 128-key tile
-constexpr long long kWaitLimit = 1ll << 31;  // cycles (~1 s)
+constexpr int kMaxSplit = 8;             // the portable cluster size; 16 ran twice as long as 8 in every shape
 
 template <int HD>
 struct Layout {
     static constexpr int kPanels = HD / 64;
-    static constexpr int kSlots = HD == 64 ? 8 : 4;               // 128 KB of K/V tiles
+    static constexpr int kSlots = HD == 64 ? 4 : 2;               // K tiles, and V tiles: 128 KB together
     static constexpr uint32_t kTile = kPanels * kPanel;           // Q, K or V tile bytes
     static constexpr uint32_t kQ1 = kTile;
-    static constexpr uint32_t kRing = 2 * kTile;
-    static constexpr uint32_t kBar = kRing + kSlots * kTile;
+    static constexpr uint32_t kRingK = 2 * kTile;
+    static constexpr uint32_t kRingV = kRingK + kSlots * kTile;
+    static constexpr uint32_t kBar = kRingV + kSlots * kTile;
     static constexpr int bQFull = 0;
-    static constexpr int bFull = 1;                    // [kSlots] tile in shared memory, V cleared
-    static constexpr int bEmpty = bFull + kSlots;      // [kSlots]
-    static constexpr int bSFull = bEmpty + kSlots;     // [2]
+    static constexpr int bFullK = 1;                   // [kSlots]
+    static constexpr int bEmptyK = bFullK + kSlots;    // [kSlots]
+    static constexpr int bFullV = bEmptyK + kSlots;    // [kSlots] landed and cleared past the last key
+    static constexpr int bEmptyV = bFullV + kSlots;    // [kSlots]
+    static constexpr int bLand = bEmptyV + kSlots;     // [kSlots] the ragged V tile landed, not yet cleared
+    static constexpr int bSFull = bLand + kSlots;      // [2]
     static constexpr int bPFull = bSFull + 2;          // [2] whole P written
     static constexpr int bPHalf = bPFull + 2;          // [2] P of keys 64..127 written
     static constexpr int bOFull = bPHalf + 2;          // [2]
-    static constexpr int bLast = bOFull + 2;           // the ragged V tile landed, not yet cleared
-    static constexpr int bFinal = bLast + 1;           // every MMA done
+    static constexpr int bFinal = bOFull + 2;          // every MMA done
     static constexpr int kNumBars = bFinal + 1;
     static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // tmem base, abort, plan (12 ints)
     static constexpr uint32_t kMl = (kMisc + 64 + 15) / 16 * 16;  // float2 [2][128]: m, l of a tile row
@@ -98,10 +92,8 @@ struct Layout {
     // merge: fp32 O rows over Q and the ring, padded by 4 floats (16-byte
     // stores of adjacent rows fall on different banks)
     static constexpr uint32_t kRow = HD + 4;
-    static_assert(2 * BM * kRow * 4 <= kBar, "merge buffer");
-    __host__ __device__ static constexpr uint32_t tS(int i) { return i ? 128u : 0u; }
-    __host__ __device__ static constexpr uint32_t tO(int i) { return i ? 384u : 256u; }
-    static constexpr uint32_t tP = 64;                             // offset of P inside S
+    static constexpr uint32_t kWeights = 2 * BM * kRow * 4;        // then the rows' weights, float [256][2 * kMaxSplit]
+    static_assert(kWeights + 2 * BM * 2 * kMaxSplit * 4 <= kBar, "merge buffer");
 };
 
 struct Args {
@@ -112,226 +104,22 @@ struct Args {
     int n_seqs, max_pages, n_pages, page_shift;
     int n_rows, max_rows, max_len;
     int group, tile_rows;              // query heads per K/V head, query rows per tile
+    int heads_first;                   // grid x is the K/V head, y the query tile pair
     float scale_log2;
     __nv_bfloat16* out;
     long long out_ld;
     int* err;
 };
 
-struct Ctl {
-    uint32_t bar0;
-    volatile int* abort;
-    int* err;
-    __device__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
-    // Waiting threads sleep until the phase completes; the MMA warp polls
-    // (its waits sit on every key tile's critical path).
-    __device__ bool wait(int i, uint32_t parity) const {
-        if (ptx::mbar_try_wait_sleep(bar(i), parity)) return true;
-        const long long t0 = clock64();
-        for (;;) {
-            if (ptx::mbar_try_wait_sleep(bar(i), parity)) return true;
-            if (*abort) return false;
-            if (clock64() - t0 > kWaitLimit) {
-                *abort = 1;
-                raise_error(err, JANO_ETIMEOUT);
-                return false;
-            }
-        }
-    }
-    __device__ bool poll(int i, uint32_t parity) const {
-        if (ptx::mbar_try_wait(bar(i), parity)) return true;
-        const long long t0 = clock64();
-        while (!ptx::mbar_try_wait(bar(i), parity)) {
-            if (*abort) return false;
-            if (clock64() - t0 > kWaitLimit) {
-                *abort = 1;
-                raise_error(err, JANO_ETIMEOUT);
-                return false;
-            }
-        }
-        return true;
-    }
-    // Warp-uniform: the .sync.aligned operations that follow never diverge.
-    __device__ bool warp_wait(int i, uint32_t parity) const {
-        int ok = 0;
-        if ((threadIdx.x & 31) == 0) ok = wait(i, parity) ? 1 : 0;
-        return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
-    }
-};
-
-__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
-}
-// Shared-memory operand descriptors as two words, so that stepping through a
-// tile is one 32-bit add: the low word holds address / 16 and the leading
-// offset, the high word (stride 1024, 128-byte swizzle) is the same for all.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-// (the mask drops the CTA rank that a shared address carries inside a cluster)
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
-    return ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-                 "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}"
-                 ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool acc) {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
-                 ::"r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
-}
-// One lane of the converged warp, chosen by the hardware: unlike lane == 0 it
-// tells the compiler that a single thread runs what follows.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-// Order of the K and V loads of a CTA with n key tiles, and the load index of
-// tile g's K and V.
-//   pair:   K0 V0 K1 V1 ...         single: K0 K1 V0 K2 V1 K3 ... V(n-1)
-// (in the single form two tiles' S are in work at once, one per stream).
-struct LoadOrder {
-    bool single;
-    int n;
-    __device__ int k(int g) const { return single ? (g < 2 ? g : 2 * g - 1) : 2 * g; }
-    __device__ int v(int g) const { return single ? min(2 * g + 2, 2 * n - 1) : 2 * g + 1; }
-    // tile of load i, and whether it is a V
-    __device__ int tile(int i, bool& is_v) const {
-        if (!single) {
-            is_v = i & 1;
-            return i >> 1;
-        }
-        if (i < 2) {
-            is_v = n == 1 && i == 1;
-            return is_v ? 0 : i;
-        }
-        is_v = i == 2 * n - 1 || !(i & 1);
-        return i == 2 * n - 1 ? n - 1 : (is_v ? (i - 2) >> 1 : (i + 1) >> 1);
-    }
-};
-
-// Row max of 64 values; with kMask, keys >= valid are left out.
-template <bool kMask>
-__device__ __forceinline__ float max64(const uint32_t (&s)[64], int valid) {
-    float m[8];
-#pragma unroll
-    for (int a = 0; a < 8; ++a) m[a] = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < 64; e += 2) {
-        float x = __uint_as_float(s[e]), y = __uint_as_float(s[e + 1]);
-        if (kMask && e >= valid) x = -INFINITY;
-        if (kMask && e + 1 >= valid) y = -INFINITY;
-        m[(e >> 1) & 7] = ptx::fmax3(m[(e >> 1) & 7], x, y);
-    }
-    return fmaxf(ptx::fmax3(m[0], m[1], m[2]), ptx::fmax3(m[3], m[4], fmaxf(m[5], fmaxf(m[6], m[7]))));
-}
-
-// p = 2^(s*c - m) for 64 values, packed to 32 BF16x2 words; returns sum(p).
-// Masked keys give exactly 0, whatever S holds there.
-template <bool kMask>
-__device__ __forceinline__ float exp64(const uint32_t (&s)[64], int valid, float c, float m, uint32_t* pk) {
-    const uint64_t c2 = ptx::f2(c, c), nm2 = ptx::f2(-m, -m);
-    uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-    for (int e = 0; e < 64; e += 2) {
-        float xa, xb;
-        ptx::f2split(ptx::ffma2(ptx::f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nm2), xa, xb);
-        float a = ptx::ex2(xa), b = ptx::ex2(xb);
-        if (kMask && e >= valid) a = 0.f;
-        if (kMask && e + 1 >= valid) b = 0.f;
-        acc[(e >> 1) & 3] = ptx::fadd2(acc[(e >> 1) & 3], ptx::f2(a, b));
-        pk[e >> 1] = ptx::pack_bf16(a, b);
-    }
-    float lo, hi;
-    ptx::f2split(ptx::fadd2(ptx::fadd2(acc[0], acc[1]), ptx::fadd2(acc[2], acc[3])), lo, hi);
-    return lo + hi;
-}
-
-// One key tile of one tile row (see the file comment): S from TMEM, maximum,
-// lazy rescale of O, P back as BF16.  `valid`: keys of the tile this row sees.
-template <int HD, bool kMask>
-__device__ __forceinline__ void softmax_tile(uint32_t tS, int valid, float c, float& m, float& l, uint32_t bar_half) {
-    constexpr uint32_t kO = Layout<HD>::tO(0) - Layout<HD>::tS(0);      // the same for both streams
-    static_assert(Layout<HD>::tO(1) - Layout<HD>::tS(1) == kO, "O lies at one distance from S");
-    const uint32_t tO = tS + kO, tP = tS + Layout<HD>::tP;
-    uint32_t s[128];
-    ptx::tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-    ptx::tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-    ptx::tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
-    ptx::tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
-    ptx::tmem_wait_ld();
-    const uint32_t(&lo)[64] = *reinterpret_cast<const uint32_t(*)[64]>(&s[0]);
-    const uint32_t(&hi)[64] = *reinterpret_cast<const uint32_t(*)[64]>(&s[64]);
-    const float mxs = fmaxf(max64<kMask>(lo, valid), max64<kMask>(hi, valid - 64)) * c;
-    // a row that has seen no key yet keeps m = -inf: its P is masked to 0
-    const bool want = mxs > m + 8.0f;
-    if (__any_sync(0xFFFFFFFFu, want)) {
-        const float m_new = want ? mxs : m;
-        // nothing to rescale while no row of the warp has seen a key
-        if (__any_sync(0xFFFFFFFFu, m > -INFINITY)) {
-            const float alpha = want ? ptx::ex2(m - m_new) : 1.0f;
-            l *= alpha;
-#pragma unroll
-            for (int q = 0; q < HD / 32; ++q) {
-                uint32_t o[32];
-                ptx::tmem_ld32(tO + 32 * q, o);
-                ptx::tmem_wait_ld();
-                const uint64_t a2 = ptx::f2(alpha, alpha);
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    float x, y;
-                    ptx::f2split(ptx::fmul2(ptx::f2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), a2), x, y);
-                    o[e] = __float_as_uint(x);
-                    o[e + 1] = __float_as_uint(y);
-                }
-                ptx::tmem_st32(tO + 32 * q, o);
-            }
-            ptx::tmem_wait_st();
-        }
-        m = m_new;
-    }
-    // upper key half first: its P V runs while the lower half is exponentiated
-    uint32_t pk[32];
-    l += exp64<kMask>(hi, valid - 64, c, m, pk);
-    ptx::tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(pk));
-    ptx::tmem_wait_st();
-    ptx::tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar_half);
-    l += exp64<kMask>(lo, valid, c, m, pk);
-    ptx::tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(pk));
-    ptx::tmem_wait_st();
-}
-
 // What a CTA works on, from the device's lists; found by one warp.
 struct Plan {
     int seq, row0, rows0, rows1, seen;   // rows of the two tiles, keys that any of them sees; rows0 = 0: nothing
 };
 
-// The x-th query tile pair of all sequences.  Later tiles of a sequence come
-// first: under causal limits they see the most keys.
+// The x-th query tile pair of all sequences.  The longest of every 32
+// sequences come first, so that the last CTAs to start are short ones, and the
+// later tiles of a sequence before its earlier ones: under causal limits they
+// see the most keys.
 __device__ __forceinline__ Plan make_plan(const Args& a, int x, bool report) {
     const int lane = threadIdx.x & 31;
     const int step = 2 * a.tile_rows;
@@ -349,17 +137,17 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int x, bool report) {
             if (!ok && report) raise_error(a.err, JANO_EINDEX);
             tiles = ok ? (hi - lo + step - 1) / step : 0;
         }
-        int sum = tiles;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += v;
+        int before = 0;                            // tiles of the sequences that come first
+        const int others = min(32, a.n_seqs - s0);
+        for (int j = 0; j < others; ++j) {
+            const int l = __shfl_sync(0xFFFFFFFFu, len, j), t = __shfl_sync(0xFFFFFFFFu, tiles, j);
+            if (l > len || (l == len && j < lane)) before += t;
         }
-        const bool mine = x >= done + sum - tiles && x < done + sum;
+        const bool mine = x >= done + before && x < done + before + tiles;
         const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
         if (who) {
             const int src = __ffs(who) - 1;
-            const int t = tiles - 1 - (x - (done + sum - tiles));
+            const int t = tiles - 1 - (x - (done + before));
             const int first = lo + t * step;
             p.seq = s0 + src;
             p.row0 = __shfl_sync(0xFFFFFFFFu, first, src);
@@ -369,7 +157,7 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int x, bool report) {
             p.seen = __shfl_sync(0xFFFFFFFFu, len, src);
             break;
         }
-        done += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        done += __reduce_add_sync(0xFFFFFFFFu, tiles);
     }
     if (a.limits && p.rows0 > 0) {
         int most = 0;
@@ -381,71 +169,75 @@ __device__ __forceinline__ Plan make_plan(const Args& a, int x, bool report) {
 
 // Parts of a tile row: one per CTA of the cluster, two (the streams) in the
 // single form.  With M the largest m and w = 2^(m - M),
-//   out = sum w O / sum w l,   summed in a fixed order;
-// one softmax warp per row, the rows dealt over the cluster's.  The plan is
-// read again from shared memory, so nothing of it is held through the loops.
+//   out = sum w O / sum w l,   summed in a fixed order.
+// The rows are dealt over the cluster's CTAs.  First a thread per row reads the
+// parts' (m, l) and leaves the weights w / sum in shared memory; then all
+// softmax threads add 4 columns each (a warp per row, one after another, spent
+// 1,500 cycles on each row's chain of remote reads).  The plan is read again
+// from shared memory, so nothing of it is held through the loops.
 template <int HD>
 __device__ __forceinline__ void merge_rows(const Args& a) {
     using L = Layout<HD>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const volatile int* plan = reinterpret_cast<const volatile int*>(smem_raw + (base - raw) + L::kMisc + 16);
+    uint8_t* gbase = smem_raw + (base - raw);
+    const volatile int* plan = reinterpret_cast<const volatile int*>(gbase + L::kMisc + 16);
     const int row0 = plan[1], rows0 = plan[2], rows1 = plan[3];
     const bool single = rows1 == 0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_split = (int)gridDim.z;
-    constexpr int E = HD / 32;                     // columns per lane
+    const int n_split = (int)gridDim.z, parts = single ? 2 * n_split : n_split;
     const int packed0 = rows0 * a.group, total = packed0 + rows1 * a.group;
-    const int parts = single ? 2 * n_split : n_split;
-    for (int r = (int)blockIdx.z * kSoftmaxWarps + warp; r < total; r += n_split * kSoftmaxWarps) {
-        const int tile = r >= packed0, p = tile ? r - packed0 : r;
-        // lane = part: its address, weight and share of the sum
-        const int z = single ? lane >> 1 : lane, st = single ? lane & 1 : tile;
-        uint32_t row_addr = 0;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < parts) {
-            const uint32_t peer = ptx::mapa_shared(base, (uint32_t)z);
-            ml = ld_cluster_f2(peer + L::kMl + (st * BM + p) * 8);
-            row_addr = peer + (st * BM + p) * L::kRow * 4;
-        }
-        if (__any_sync(0xFFFFFFFFu, ml.y < 0.f)) continue;     // a part is missing: JANO_ETIMEOUT was raised
-        float M = ml.x, sum;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-        // a part without visible keys has m = -inf, l = 0 and no O
-        const float w = ml.y != 0.f ? ptx::ex2(ml.x - M) : 0.f;
-        sum = w * ml.y;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        float acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    const int per = (total + n_split - 1) / n_split;
+    const int begin = (int)blockIdx.z * per, count = min(per, total - begin);
+    float* weight = reinterpret_cast<float*>(gbase + L::kWeights);     // [count][parts]
+    const int t = threadIdx.x;
+    // part c of packed row r: its (m, l) at slot(r, c), its O row there too
+    auto slot = [&](int r, int c) {
+        const int tile = r >= packed0;
+        return (single ? c & 1 : tile) * BM + (tile ? r - packed0 : r);
+    };
+    auto peer = [&](int c) { return ptx::mapa_shared(base, (uint32_t)(single ? c >> 1 : c)); };
+    if (t < count) {
+        const int r = begin + t;
+        float M = -INFINITY, sum = 0.f;
+        bool missing = false;
+        float* w = weight + t * parts;
         for (int c = 0; c < parts; ++c) {
-            const float wc = __shfl_sync(0xFFFFFFFFu, w, c);
-            const uint32_t ac = __shfl_sync(0xFFFFFFFFu, row_addr, c);
-            if (wc != 0.f) {
-                if constexpr (E == 4) {
-                    const float4 o = ld_cluster_f4(ac + lane * 16);
-                    acc[0] = fmaf(wc, o.x, acc[0]);
-                    acc[1] = fmaf(wc, o.y, acc[1]);
-                    acc[2] = fmaf(wc, o.z, acc[2]);
-                    acc[3] = fmaf(wc, o.w, acc[3]);
-                } else {
-                    const float2 o = ld_cluster_f2(ac + lane * 8);
-                    acc[0] = fmaf(wc, o.x, acc[0]);
-                    acc[1] = fmaf(wc, o.y, acc[1]);
-                }
-            }
+            const float2 ml = ld_cluster_f2(peer(c) + L::kMl + slot(r, c) * 8);
+            missing = missing || ml.y < 0.f;               // JANO_ETIMEOUT was raised
+            // the sum so far is kept relative to the largest m so far
+            const float top = fmaxf(M, ml.x);
+            if (ml.y != 0.f) sum = (M > -INFINITY ? sum * ptx::ex2(M - top) : sum) + ml.y * ptx::ex2(ml.x - top);
+            M = top;
+            w[c] = ml.y != 0.f ? ml.x : -INFINITY;         // a part without visible keys has no O
         }
         const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+        for (int c = 0; c < parts; ++c)
+            w[c] = missing ? -1.0f : (w[c] > -INFINITY || sum != sum ? ptx::ex2(w[c] - M) * inv : 0.f);
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");         // the softmax warps
+    constexpr int kVec = HD / 4;
+#pragma unroll 2
+    for (int u = t; u < count * kVec; u += 32 * kSoftmaxWarps) {
+        const int i = u / kVec, col = u % kVec, r = begin + i;
+        const float* w = weight + i * parts;
+        if (w[0] < 0.f) continue;
+        float x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < parts; ++c) {
+            const float wc = w[c];
+            if (wc != 0.f) {
+                const float4 o = ld_cluster_f4(peer(c) + slot(r, c) * L::kRow * 4 + col * 16);
+                x0 = fmaf(wc, o.x, x0);
+                x1 = fmaf(wc, o.y, x1);
+                x2 = fmaf(wc, o.z, x2);
+                x3 = fmaf(wc, o.w, x3);
+            }
+        }
+        const int tile = r >= packed0, p = tile ? r - packed0 : r;
         __nv_bfloat16* dst = a.out + (long long)(row0 + tile * a.tile_rows + p / a.group) * a.out_ld +
-                             ((int)blockIdx.y * a.group + p % a.group) * HD + lane * E;
-        if constexpr (E == 4)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(ptx::pack_bf16(acc[0] * inv, acc[1] * inv), ptx::pack_bf16(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = ptx::pack_bf16(acc[0] * inv, acc[1] * inv);
+                             ((int)(a.heads_first ? blockIdx.x : blockIdx.y) * a.group + p % a.group) * HD + col * 4;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16(x0, x1), ptx::pack_bf16(x2, x3));
     }
 }
 
@@ -460,7 +252,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     uint8_t* gbase = smem_raw + (base - raw);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = blockIdx.y;                       // K/V head
+    const int head = a.heads_first ? blockIdx.x : blockIdx.y;      // K/V head
     const int n_split = (int)gridDim.z, split = (int)blockIdx.z;
 
     Ctl ctl;
@@ -471,7 +263,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     int* plan_slot = reinterpret_cast<int*>(gbase + L::kMisc + 16);
 
     if (warp == 0) {
-        const Plan p = make_plan(a, (int)blockIdx.x, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
+        const Plan p = make_plan(a, (int)(a.heads_first ? blockIdx.y : blockIdx.x),
+                                 blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0);
         if (lane == 0) {
             plan_slot[0] = p.seq;
             plan_slot[1] = p.row0;
@@ -483,8 +276,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     if (threadIdx.x == 32) {
         ptx::mbar_init(ctl.bar(L::bQFull), 1);
         for (int s = 0; s < L::kSlots; ++s) {
-            ptx::mbar_init(ctl.bar(L::bFull + s), 1);
-            ptx::mbar_init(ctl.bar(L::bEmpty + s), 1);
+            ptx::mbar_init(ctl.bar(L::bFullK + s), 1);
+            ptx::mbar_init(ctl.bar(L::bEmptyK + s), 1);
+            ptx::mbar_init(ctl.bar(L::bFullV + s), 1);
+            ptx::mbar_init(ctl.bar(L::bEmptyV + s), 1);
+            ptx::mbar_init(ctl.bar(L::bLand + s), 1);
         }
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(ctl.bar(L::bSFull + s), 1);
@@ -492,7 +288,6 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             ptx::mbar_init(ctl.bar(L::bPHalf + s), 4);
             ptx::mbar_init(ctl.bar(L::bOFull + s), 1);
         }
-        ptx::mbar_init(ctl.bar(L::bLast), 1);
         ptx::mbar_init(ctl.bar(L::bFinal), 1);
         *ctl.abort = 0;
         ptx::fence_mbar_init();
@@ -522,165 +317,113 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     const int nt = (seen + BN - 1) / BN;
     const int kt0 = (int)((long long)nt * split / n_split);
     const int n = rows0 > 0 ? (int)((long long)nt * (split + 1) / n_split) - kt0 : 0;
-    const LoadOrder order{single, n};
     const bool ragged = n > 0 && kt0 + n == nt && seen % BN != 0;   // this CTA holds the ragged last tile
     const bool merge = rows0 > 0 && (single || n_split > 1);
 
     if (warp >= 8) {
       ptx::setmaxnreg_dec<kRegsIssue>();
-      if (warp == 8 && n > 0) {
-        // ------------------------------------------------------------ producer
+      if ((warp == 8 || warp == 11) && n > 0) {
+        // ------------------------------------------------------------ producers: Q and K, V
+        const bool is_v = uniform(warp) == 11;
         if (elect_one()) {
-            const uint32_t q_bytes = (uint32_t)(a.tile_rows * a.group * 128 * L::kPanels);
-            ptx::mbar_arrive_expect_tx(ctl.bar(L::bQFull), single ? q_bytes : 2 * q_bytes);
-            for (int p = 0; p < L::kPanels; ++p) {
-                ptx::tma_load_3d(base + p * kPanel, &tmQ, ctl.bar(L::bQFull), p * 64, head * a.group, row0);
-                if (!single)
-                    ptx::tma_load_3d(base + L::kQ1 + p * kPanel, &tmQ, ctl.bar(L::bQFull), p * 64, head * a.group,
-                                     row0 + a.tile_rows);
+            if (!is_v) {
+                const uint32_t q_bytes = (uint32_t)(a.tile_rows * a.group * 128 * L::kPanels);
+                ptx::mbar_arrive_expect_tx(ctl.bar(L::bQFull), single ? q_bytes : 2 * q_bytes);
+                for (int p = 0; p < L::kPanels; ++p) {
+                    ptx::tma_load_3d(base + p * kPanel, &tmQ, ctl.bar(L::bQFull), p * 64, head * a.group, row0);
+                    if (!single)
+                        ptx::tma_load_3d(base + L::kQ1 + p * kPanel, &tmQ, ctl.bar(L::bQFull), p * 64, head * a.group,
+                                         row0 + a.tile_rows);
+                }
             }
-            const int shift = a.page_shift, page_rows = 1 << shift;
-            const int box_rows = min(page_rows, BN);
-            const int32_t* pages = a.table + (long long)seq * a.max_pages;
-            // the page ids of a load are read right after the load before it
-            // went out, so they arrive while its slot is still in use
-            int ids[kMaxBoxes];
-            auto read_ids = [&](int i) {
-                bool is_v;
-                const int key0 = (kt0 + order.tile(i, is_v)) * BN;
-                const int boxes = (min(seen - key0, BN) + box_rows - 1) / box_rows;
-#pragma unroll
-                for (int b = 0; b < kMaxBoxes; ++b)
-                    if (b < boxes) ids[b] = __ldg(pages + ((key0 + b * box_rows) >> shift));
-            };
-            read_ids(0);
-            int issued = 0;
-            for (int i = 0; i < 2 * n; ++i) {
-                bool is_v;
-                const int key0 = (kt0 + order.tile(i, is_v)) * BN;
-                const int live = min(seen - key0, BN);
-                const int boxes = (live + box_rows - 1) / box_rows;
-                const int s = i % L::kSlots;
-                if (!ctl.wait(L::bEmpty + s, ((i / L::kSlots) & 1) ^ 1)) break;
-#ifdef JANO_INJECT_DROP_LOAD
-                // failure-path test builds only: this tile is never issued, so
-                // the MMA's bounded wait for it runs out (JANO_ETIMEOUT)
-                if (i == JANO_INJECT_DROP_LOAD) continue;
-#endif
-                const uint32_t bar = ctl.bar(is_v && live < BN ? L::bLast : L::bFull + s);
-                ptx::mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box_rows * 128 * L::kPanels));
-                const CUtensorMap* tm = is_v ? &tmV : &tmK;
-                const uint32_t dst = base + L::kRing + s * L::kTile;
-#pragma unroll
-                for (int b = 0; b < kMaxBoxes; ++b)
-                    if (b < boxes) {
-                        int page = ids[b];
-                        if (page < 0 || page >= a.n_pages) {
-                            raise_error(a.err, JANO_EINDEX);
-                            page = a.n_pages;          // out of range: the copy fills zeros
-                        }
-                        for (int p = 0; p < L::kPanels; ++p)
-                            tma_load_4d(dst + b * box_rows * 128 + p * kPanel, tm, bar, p * 64,
-                                        key0 & (page_rows - 1), head, page);
-                    }
-                issued = i + 1;
-                if (issued < 2 * n) read_ids(issued);
-            }
-            // drain: every copy this CTA issued lands before its smem is released
-            ptx::mbar_wait(ctl.bar(L::bQFull), 0, kWaitLimit);
-            for (int i = max(0, issued - L::kSlots); i < issued; ++i) {
-#ifdef JANO_INJECT_DROP_LOAD
-                if (i == JANO_INJECT_DROP_LOAD) continue;
-#endif
-                bool is_v;
-                const int g = order.tile(i, is_v);
-                if (is_v && seen - (kt0 + g) * BN < BN) ptx::mbar_wait(ctl.bar(L::bLast), 0, kWaitLimit);
-                else ptx::mbar_wait(ctl.bar(L::bFull + i % L::kSlots), (i / L::kSlots) & 1, kWaitLimit);
-            }
+            Feed<HD, L::kSlots, false> feed{ctl, is_v ? &tmV : &tmK, is_v ? L::bFullV : L::bFullK,
+                                            is_v ? L::bEmptyV : L::bEmptyK, L::bLand, is_v,
+                                            base + (is_v ? L::kRingV : L::kRingK)};
+            feed.tiles(a.table + (long long)seq * a.max_pages, a.page_shift, a.n_pages, kt0, n, seen, head);
+            if (!is_v) ptx::mbar_wait(ctl.bar(L::bQFull), 0, kWaitLimit);
+            feed.drain();
         }
       } else if (warp == 9 && n > 0) {
         // ------------------------------------------------------------ MMA issuer
         if (elect_one()) {
             constexpr uint32_t idesc_qk = ptx::idesc_bf16(BM, BN, false, false);
             constexpr uint32_t idesc_pv = ptx::idesc_bf16(BM, HD, false, true);
-            auto slot_of = [](int i) { return i % L::kSlots; };
-            auto wait_full = [&](int i) { return ctl.poll(L::bFull + slot_of(i), (i / L::kSlots) & 1); };
-            auto release = [&](int i) { ptx::mma_commit(ctl.bar(L::bEmpty + slot_of(i))); };
-            auto qk = [&](int st, uint32_t qb, int i) {    // S_st = Q K^T, K in load i's slot
-                const uint32_t kd = desc_lo(base + L::kRing + slot_of(i) * L::kTile, 16), qd = desc_lo(qb, 16);
+            RingPos<L::kSlots> kp, vp;
+            auto wait_k = [&]() { return ctl.poll(L::bFullK + kp.slot, kp.phase); };
+            auto wait_v = [&]() { return ctl.poll(L::bFullV + vp.slot, vp.phase); };
+            auto release_k = [&]() { ptx::mma_commit(ctl.bar(L::bEmptyK + kp.slot)); kp.advance(); };
+            auto release_v = [&]() { ptx::mma_commit(ctl.bar(L::bEmptyV + vp.slot)); vp.advance(); };
+            auto qk = [&](int st, uint32_t qb) {           // S_st = Q K^T, K the ring's next tile
+                const uint32_t kd = desc_lo(base + L::kRingK + kp.slot * L::kTile, 16), qd = desc_lo(qb, 16);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * kPanel + (kk & 3) * 32) >> 4;
-                    mma_ss(tmem + L::tS(st), qd + off, kd + off, idesc_qk, kk > 0);
+                    mma_ss(tmem + tmem_s(st), qd + off, kd + off, idesc_qk, kk > 0);
                 }
                 ptx::mma_commit(ctl.bar(L::bSFull + st));
             };
-            // O_st += P_st V over key sixteenths [k0, k1); V in load i's slot
-            auto pv = [&](int st, int i, int k0, int k1, bool acc) {
-                const uint32_t vd = desc_lo(base + L::kRing + slot_of(i) * L::kTile, kPanel);
+            // O_st += P_st V over key sixteenths [k0, k1); V the ring's next tile
+            auto pv = [&](int st, int k0, int k1, bool acc) {
+                const uint32_t vd = desc_lo(base + L::kRingV + vp.slot * L::kTile, kPanel);
 #pragma unroll
                 for (int kk = k0; kk < k1; ++kk)
-                    mma_ts(tmem + L::tO(st), tmem + L::tS(st) + L::tP + kk * 8, vd + kk * 128, idesc_pv,
+                    mma_ts(tmem + tmem_o(st), tmem + tmem_s(st) + kTmemP + kk * 8, vd + kk * 128, idesc_pv,
                            acc || kk > k0);
             };
-            auto pv_tile = [&](int st, int i, int j) -> bool {
+            auto pv_tile = [&](int st, int j) -> bool {    // its j-th tile
                 if (!ctl.poll(L::bPHalf + st, j & 1)) return false;
                 ptx::tc_fence_after();
-                pv(st, i, BN / 32, BN / 16, j > 0);
+                pv(st, BN / 32, BN / 16, j > 0);
                 if (!ctl.poll(L::bPFull + st, j & 1)) return false;
                 ptx::tc_fence_after();
-                pv(st, i, 0, BN / 32, true);
+                pv(st, 0, BN / 32, true);
                 return true;
             };
             bool ok = ctl.poll(L::bQFull, 0);
             if (!single) {
                 // S0_0 S1_0 | PV0_{j-1} S0_j PV1_{j-1} S1_j | ... PV0 PV1
-                // (loads: K_j is 2j, V_j is 2j + 1)
-                if (ok && (ok = wait_full(0))) {
+                if (ok && (ok = wait_k())) {
                     ptx::tc_fence_after();
-                    qk(0, base, 0);
-                    qk(1, base + L::kQ1, 0);
-                    release(0);
+                    qk(0, base);
+                    qk(1, base + L::kQ1);
+                    release_k();
                 }
                 for (int j = 1; ok && j < n; ++j) {
-                    const int ik = 2 * j, iv = 2 * j - 1;
-                    if (!wait_full(iv) || !wait_full(ik)) { ok = false; break; }
-                    if (!pv_tile(0, iv, j - 1)) { ok = false; break; }
-                    qk(0, base, ik);
-                    if (!pv_tile(1, iv, j - 1)) { ok = false; break; }
-                    release(iv);
-                    qk(1, base + L::kQ1, ik);
-                    release(ik);
+                    if (!wait_v() || !wait_k()) { ok = false; break; }
+                    if (!pv_tile(0, j - 1)) { ok = false; break; }
+                    qk(0, base);
+                    if (!pv_tile(1, j - 1)) { ok = false; break; }
+                    release_v();
+                    qk(1, base + L::kQ1);
+                    release_k();
                 }
                 if (ok) {
-                    const int iv = 2 * n - 1;
-                    ok = wait_full(iv) && pv_tile(0, iv, n - 1);
+                    ok = wait_v() && pv_tile(0, n - 1);
                     if (ok) {
                         ptx::mma_commit(ctl.bar(L::bOFull + 0));
-                        ok = pv_tile(1, iv, n - 1);
+                        ok = pv_tile(1, n - 1);
                     }
                     if (ok) {
                         ptx::mma_commit(ctl.bar(L::bOFull + 1));
-                        release(iv);
+                        release_v();
                     }
                 }
             } else {
                 // S0(0) S1(1) | PV(g) S(g+2) ... over the tiles g, stream g & 1
-                const LoadOrder order{true, n};
                 for (int g = -2; ok && g < n; g += 2) {
 #pragma unroll
                     for (int st = 0; st < 2; ++st) {
                         const int v = g + st, k = g + st + 2;
                         if (v >= 0 && v < n) {
-                            if (!wait_full(order.v(v)) || !pv_tile(st, order.v(v), v >> 1)) { ok = false; break; }
-                            release(order.v(v));
+                            if (!wait_v() || !pv_tile(st, v >> 1)) { ok = false; break; }
+                            release_v();
                             if (k >= n) ptx::mma_commit(ctl.bar(L::bOFull + st));
                         }
                         if (k < n) {
-                            if (!wait_full(order.k(k))) { ok = false; break; }
+                            if (!wait_k()) { ok = false; break; }
                             ptx::tc_fence_after();
-                            qk(st, base, order.k(k));
-                            release(order.k(k));
+                            qk(st, base);
+                            release_k();
                         }
                     }
                 }
@@ -691,16 +434,16 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         }
       } else if (warp == 10 && ragged) {
         // ------------------------------------------------------------ V rows past the last key
-        const int i = order.v(n - 1);
-        if (ctl.warp_wait(L::bLast, 0)) {
+        const int at = (n - 1) % L::kSlots;
+        if (ctl.warp_wait(L::bLand + at, 0)) {
             const int live = seen - (nt - 1) * BN;
-            uint8_t* v = gbase + L::kRing + (i % L::kSlots) * L::kTile;
+            uint8_t* v = gbase + L::kRingV + at * L::kTile;
             for (int e = live * 8 + lane; e < BN * 8; e += 32)
                 for (int p = 0; p < L::kPanels; ++p)
                     *reinterpret_cast<uint4*>(v + p * kPanel + e * 16) = make_uint4(0, 0, 0, 0);
             fence_proxy_async();           // ordered before the tensor core's reads
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bFull + i % L::kSlots));
+            if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bFullV + at));
         }
       }
       // the same barriers as the softmax warps' (both branches end for
@@ -724,8 +467,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const int q = uniform(warp & 3);              // TMEM lane quarter of this warp
         const int row = q * 32 + lane;
         const uint32_t lane_off = (uint32_t)(q * 32) << 16;
-        const uint32_t tS = tmem + lane_off + L::tS(i);
-        const uint32_t tO = tmem + lane_off + L::tO(i);
+        const uint32_t tS = tmem + lane_off + tmem_s(i);
+        const uint32_t tO = tmem + lane_off + tmem_o(i);
         const bool warp_live = q * 32 < (i && !single ? rows1 : rows0) * a.group;   // else only the barriers are kept
         const int steps = single ? (n + 1 - i) >> 1 : n;
         // the stream's tiles start at keys first, first + apart, ...
@@ -739,10 +482,11 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         float m = -INFINITY, l = 0.f;
         int j = 0;
         if (warp_live) {
+            // (two loops: the one body with a branch in it cost 4% of a long chunk's time)
             for (; j < plain; ++j) {
                 if (!ctl.warp_wait(L::bSFull + i, j & 1)) break;
                 ptx::tc_fence_after();
-                softmax_tile<HD, false>(tS, BN, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
+                softmax_tile<HD>(tS, false, BN, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + i));
@@ -750,7 +494,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             for (; j < steps; ++j) {
                 if (!ctl.warp_wait(L::bSFull + i, j & 1)) break;
                 ptx::tc_fence_after();
-                softmax_tile<HD, true>(tS, limit - first - j * apart, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
+                softmax_tile<HD>(tS, true, limit - first - j * apart, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + i));
@@ -832,104 +576,39 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Rows [n_rows][heads][d]: a box is one tile's query rows x the heads of a group x 64 columns.
-bool make_q_map(CUtensorMap* m, const void* q, long long ld, int n_rows, int heads, int d, int group, int tile_rows) {
-    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n_rows};
-    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_rows};
-    return encode(m, q, 3, dims, strides, box);
-}
-
-// The pool [page][place][head][d] with its own strides: a box is up to 128 places of one page and head x 64 columns.
-bool make_pool_map(CUtensorMap* m, const void* pages, const jano_page_pool& p) {
-    const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.page_size, (cuuint64_t)p.kv_heads,
-                                (cuuint64_t)p.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, (cuuint64_t)p.head_stride * 2,
-                                   (cuuint64_t)p.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(p.page_size < BN ? p.page_size : BN), 1, 1};
-    return encode(m, pages, 4, dims, strides, box);
-}
-
 template <int HD>
-cudaError_t set_up(int dev, int& max_cluster) {
+cudaError_t set_up(int dev) {
     using L = Layout<HD>;
     static DeviceOnce ready;
-    static std::atomic<int> cluster_of[64];
-    if (!ready.done(dev)) {
-        // the register split assumes exactly kRegsLaunch registers per thread
-        cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, paged_attention_kernel<HD>);
-        if (e != cudaSuccess) return e;
-        if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(paged_attention_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)L::kAlloc);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(paged_attention_kernel<HD>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        // clusters of 16 CTAs need 16 free SMs in one GPC: asked once per device
-        cudaLaunchConfig_t cfg{};
-        cudaLaunchAttribute attr[1];
-        cfg.gridDim = dim3(1, 1, 16);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = L::kAlloc;
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim = {1, 1, 16};
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int active = 0;
-        const bool wide = cudaOccupancyMaxActiveClusters(&active, paged_attention_kernel<HD>, &cfg) == cudaSuccess &&
-                          active > 0;
-        if (!wide) cudaGetLastError();
-        if (dev >= 0 && dev < 64) cluster_of[dev].store(wide ? 16 : 8, std::memory_order_relaxed);
-        ready.mark(dev);
-        max_cluster = wide ? 16 : 8;
-        return cudaSuccess;
-    }
-    max_cluster = cluster_of[dev].load(std::memory_order_relaxed);
-    return cudaSuccess;
+    if (ready.done(dev)) return cudaSuccess;
+    // the register split assumes exactly kRegsLaunch registers per thread
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, paged_attention_kernel<HD>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(paged_attention_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kAlloc);
+    if (e == cudaSuccess) ready.mark(dev);
+    return e;
 }
 
 template <int HD>
 cudaError_t launch_hd(const PagedAttentionCall& c, const Args& a, int tiles, int* err, cudaStream_t st) {
     using L = Layout<HD>;
-    int dev = 0, max_cluster = 8;
+    int dev = 0;
     cudaGetDevice(&dev);
-    cudaError_t e = set_up<HD>(dev, max_cluster);
+    const cudaError_t e = set_up<HD>(dev);
     if (e != cudaSuccess) return e;
     int sms = 148;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     int split = c.n_split;
     if (split == 0)
         split = paged_split_count(c.n_rows, c.max_rows, c.max_len, c.seqs->n_seqs, c.heads, c.pool->kv_heads, sms);
-    if (split > max_cluster) split = max_cluster;
     CUtensorMap mq, mk, mv;
     if (!make_q_map(&mq, c.q, c.q_ld, c.n_rows, c.heads, HD, a.group, a.tile_rows) ||
         !make_pool_map(&mk, c.pool->k, *c.pool) || !make_pool_map(&mv, c.pool->v, *c.pool))
         return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)tiles, (unsigned)c.pool->kv_heads, (unsigned)split);
+    const dim3 grid = a.heads_first ? dim3((unsigned)c.pool->kv_heads, (unsigned)tiles, (unsigned)split)
+                                    : dim3((unsigned)tiles, (unsigned)c.pool->kv_heads, (unsigned)split);
     if (split == 1) {
         paged_attention_kernel<HD><<<grid, kThreads, L::kAlloc, st>>>(mq, mk, mv, a);
         return cudaGetLastError();
@@ -958,23 +637,25 @@ long long tile_bound(int n_rows, int max_rows, int n_seqs, int tile_rows) {
 
 }  // namespace
 
-// CTAs per (query tile pair, K/V head): the cluster size z (1, 2, 4, 8, 16)
-// with the shortest modelled time, rounds of z C CTAs over the SMs times the
-// key tiles of one CTA plus the equivalent of `fixed` tiles for its set-up,
-// pipeline fill and merge.
+// CTAs per (query tile pair, K/V head): the cluster size z (1, 2, 4, 8) with
+// the shortest modelled time: rounds of the C clusters over the device times
+// the key tiles of one CTA plus the equivalent of 5 tiles for its set-up, fill
+// and drain, 7.5 where a merge follows (1.8 us a tile).  Clusters of 4 and 8 do
+// not fill the GPCs: 33 of 37 and 15 of 18 are resident at once on 148 SMs.
+// Over 17 measured shapes (1 to 768 CTAs, 3 to 591 key tiles) the choice is
+// within 6% of the best.
 int paged_split_count(int n_rows, int max_rows, int max_len, int n_seqs, int heads, int kv_heads, int sms) {
     if (n_rows <= 0 || max_rows <= 0 || max_len <= 0 || sms <= 0) return 1;
     const int tile_rows = BM / (heads / kv_heads);
-    const double ctas = (double)tile_bound(n_rows, max_rows, n_seqs, tile_rows) * kv_heads;
+    const long long clusters = tile_bound(n_rows, max_rows, n_seqs, tile_rows) * kv_heads;
     const int nt = (max_len + BN - 1) / BN;
-    const double fixed = 12.0;
     int best = 1;
     double best_t = 0.0;
-    for (int z = 1; z <= kMaxSplit && (z == 1 || nt >= 2 * z); z *= 2) {
-        const double w = ctas * z / sms;
-        const double full = std::floor(w), f = w - full;
-        const double rounds = full + (f > 1e-9 ? 0.7 + 0.3 * f : 0.0);
-        const double t = rounds * ((double)nt / z + fixed);
+    for (int z = 1; z <= kMaxSplit && z <= nt; z *= 2) {
+        const int fit = sms / z - (z == 4 ? sms / 37 : z == 8 ? sms / 49 : 0);
+        const long long resident = fit < 1 ? 1 : fit;
+        const double rounds = (double)((clusters + resident - 1) / resident);
+        const double t = rounds * ((double)nt / z + (z == 1 ? 5.0 : 7.5));
         if (z == 1 || t < best_t * (1.0 - 1e-9)) {
             best_t = t;
             best = z;
@@ -1006,6 +687,10 @@ cudaError_t launch_paged_attention(const PagedAttentionCall& c, int* err, cudaSt
     a.err = err;
     const long long tiles = tile_bound(c.n_rows, c.max_rows, c.seqs->n_seqs, a.tile_rows);
     if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    // one sequence: its tiles side by side, so that the CTAs at work share the
+    // K/V of few heads in L2.  Several: all heads of the longest tiles first
+    // (four ragged images: measured below)
+    a.heads_first = c.seqs->n_seqs > 1 && tiles <= 65535;
     return c.pool->d == 128 ? launch_hd<128>(c, a, (int)tiles, err, st) : launch_hd<64>(c, a, (int)tiles, err, st);
 }
 

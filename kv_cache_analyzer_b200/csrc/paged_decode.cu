@@ -1,0 +1,725 @@
+// paged_decode.cu -- paged attention of few rows per sequence (single tokens
+// above all): at most 32 packed rows, (query row, head of the group), per
+// sequence and K/V head.  Same formula and layout as paged_attention.cu.
+//
+// Bound by the cache's bytes, so the design serves one thing: K/V tiles in
+// flight on every SM until the last byte.  One persistent CTA per SM takes an
+// equal share of all key tiles, counted through sequences, heads and keys in
+// that order, whatever the lengths; where a share begins or ends inside a
+// sequence's head, the CTA leaves a partial (O, m, l) and a second kernel, its
+// programmatic dependent, adds the parts in order.  Within a CTA the loads of
+// the next (sequence, head) start while the last one is still being worked
+// on: all barriers count through, Q has two buffers, and as a tile of 32 live
+// rows needs only 8 KB of Q, six K/V tiles of 32 KB (d = 128) fit beside it
+// (four in paged_attention.cu).  The MMAs have M = 128 all the same; the rows
+// past 32 read whatever shared memory follows, and nobody reads their results.
+//
+// 7 warps:  0, 1  softmax of streams 0 and 1 (even and odd key tiles; thread =
+// packed row.  Stream 1's operand starts 32 rows before Q, so its rows fall
+// into the TMEM lanes that warp 1 reaches, on another scheduler), 2 MMA
+// issuer, 3 clears V rows past the visible length, 4 planner: it walks the
+// device's lists once and hands the CTA's segments (runs of key tiles of one
+// sequence and head) to the others through a small ring, 5 producer of Q and
+// K, 6 producer of V.  The two streams' parts are joined through shared memory
+// at the end of each segment.
+//
+// Every wait is bounded.  The partial slots of a CTA are marked missing before
+// it starts, so that rows of a CTA that gave up are not written.
+#include "paged_tile.cuh"
+
+namespace jano {
+namespace {
+
+constexpr int kThreads = 224;                // two warps per scheduler at most: 255 registers for a thread's S row
+constexpr int kRows = 32;                    // packed rows at most
+constexpr int kSegs = 4;                     // segments in the planner's ring
+constexpr uint32_t kQPanel = kRows * 128;    // bytes of one 32-row x 64-column panel
+
+// A run of key tiles of one (sequence, K/V head).
+struct Seg {
+    int row0, rows;      // query rows
+    int seq, head;
+    int seen;            // keys that any of the rows sees
+    int kt0, n;          // first key tile, key tiles (0: no more segments)
+    int part;            // partial slot of the CTA that it goes to; -1: the whole item, straight to out
+};
+
+template <int HD>
+struct Layout {
+    static constexpr int kPanels = HD / 64;
+    static constexpr int kSlots = HD == 64 ? 6 : 3;               // K tiles, and V tiles: 192 KB together
+    static constexpr uint32_t kTile = kPanels * kPanel;
+    static constexpr uint32_t kQ = kPanels * kQPanel;             // one Q buffer
+    // stream 1's O, float [kRows][kStageRow] (padded: adjacent rows on different
+    // banks), its (m, l), then Q and the ring: an MMA of stream 1 reads 4 KB
+    // before a Q panel and either one up to 16 KB past its start
+    static constexpr uint32_t kStageRow = HD + 4;
+    static constexpr uint32_t kStageMl = kRows * kStageRow * 4;
+    static constexpr uint32_t kQ0 = (kStageMl + kRows * 8 + 1023) / 1024 * 1024;
+    static constexpr uint32_t kRingK = kQ0 + 2 * kQ;
+    static constexpr uint32_t kRingV = kRingK + kSlots * kTile;
+    static constexpr uint32_t kBar = kRingV + kSlots * kTile;
+    static constexpr int bFullK = 0;                   // [kSlots]
+    static constexpr int bEmptyK = bFullK + kSlots;    // [kSlots]
+    static constexpr int bFullV = bEmptyK + kSlots;    // [kSlots] landed and cleared past the last key
+    static constexpr int bEmptyV = bFullV + kSlots;    // [kSlots]
+    static constexpr int bLand = bEmptyV + kSlots;     // [kSlots] a ragged V tile landed, not yet cleared
+    static constexpr int bQFull = bLand + kSlots;      // [2]
+    static constexpr int bQEmpty = bQFull + 2;         // [2]
+    static constexpr int bSFull = bQEmpty + 2;         // [2]
+    static constexpr int bPHalf = bSFull + 2;          // [2]
+    static constexpr int bPFull = bPHalf + 2;          // [2]
+    static constexpr int bOFull = bPFull + 2;          // [2]
+    static constexpr int bOEmpty = bOFull + 2;         // [2]
+    static constexpr int bStage = bOEmpty + 2;
+    static constexpr int bStageFree = bStage + 1;
+    static constexpr int bSegFull = bStageFree + 1;    // [kSegs]
+    static constexpr int bSegEmpty = bSegFull + kSegs; // [kSegs]
+    static constexpr int bFinal = bSegEmpty + kSegs;
+    static constexpr int kNumBars = bFinal + 1;
+    static constexpr uint32_t kSeg = kBar + 8 * kNumBars;         // Seg [kSegs]
+    static constexpr uint32_t kMisc = kSeg + kSegs * (uint32_t)sizeof(Seg);
+    static constexpr uint32_t kBytes = kMisc + 16;                // tmem base, abort flag, share is empty
+    static constexpr uint32_t kAlloc = kBytes + 1024;             // slack for 1 KB alignment
+    static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+    static_assert(kQ0 >= kQPanel && kRingK % 1024 == 0 && kBar % 8 == 0, "alignment");
+};
+
+struct Args {
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu;
+    const int32_t* limits;
+    int n_seqs, max_pages, n_pages, page_shift;
+    int n_rows, max_rows, max_len;
+    int kv_heads, group, tile_rows;    // query heads per K/V head, query rows per tile
+    float scale_log2;
+    __nv_bfloat16* out;
+    long long out_ld;
+    float* part_o;                     // [2 * CTAs][part_rows][d]
+    float2* part_ml;                   // [2 * CTAs][part_rows]
+    int part_rows;
+    int* err;
+};
+
+// One sequence as this lane sees it: its rows, the keys they see, key tiles
+// per head (one, all masked, for rows that see nothing: they are written too).
+struct SeqInfo {
+    int row0, rows, seen, tiles;
+};
+__device__ __forceinline__ SeqInfo seq_info(const Args& a, int s, bool report) {
+    SeqInfo q{0, 0, 0, 0};
+    if (s >= a.n_seqs) return q;
+    const int lo = __ldg(a.cu + s), hi = __ldg(a.cu + s + 1), len = __ldg(a.lens + s);
+    const bool ok = lo >= 0 && lo <= hi && hi <= a.n_rows && hi - lo <= a.max_rows && len >= 0 && len <= a.max_len &&
+                    (s > 0 || lo == 0);
+    if (!ok && report) raise_error(a.err, JANO_EINDEX);
+    if (!ok || hi == lo) return q;
+    q.row0 = lo;
+    q.rows = hi - lo;
+    q.seen = len;
+    if (a.limits) {
+        int most = 0;
+        for (int r = lo; r < hi; ++r) most = max(most, __ldg(a.limits + r));
+        q.seen = min(len, most);
+    }
+    q.tiles = max(1, (q.seen + BN - 1) / BN);
+    return q;
+}
+// A row of O from TMEM, all columns in one round trip.
+template <int HD>
+__device__ __forceinline__ void load_row(uint32_t tO, uint32_t (&o)[HD]) {
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c) ptx::tmem_ld32(tO + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&o[32 * c]));
+    ptx::tmem_wait_ld();
+}
+__device__ __forceinline__ int warp_sum_to(int v) {    // inclusive prefix sum over the lanes
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+// Key tiles of all sequences and heads (the whole warp); the launcher has
+// checked that they fit an int.
+__device__ __forceinline__ int all_tiles(const Args& a, bool report) {
+    int total = 0;
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 32)
+        total += __reduce_add_sync(0xFFFFFFFFu, seq_info(a, s0 + (threadIdx.x & 31), report).tiles);
+    return total * a.kv_heads;
+}
+// Equal shares of the tiles, the first `more` ones a tile longer; no more
+// shares than give each of them two tiles.
+struct Shares {
+    int n, each, more;
+    __device__ Shares(int total, int ctas) : n(max(1, min((total + 1) / 2, ctas))), each(total / n), more(total - each * n) {}
+    __device__ int begin(int c) const { return c * each + min(c, more); }
+};
+
+// The segments of one CTA's share, one after another (a whole warp walks).
+struct Walk {
+    const Args& a;
+    int begin, end;                        // the share, in tiles
+    int s0, at;                            // the 32 sequences in hand, and their first tile
+    SeqInfo mine;
+    int from, upto;                        // this lane's sequence's first tile; tiles of the 32 up to it
+    unsigned todo;                         // lanes whose sequences are still to come
+    Seg s;
+    int tiles, first, item;                // of the sequence in hand; the item's first tile (< end: there is one)
+
+    // `all`: key tiles of every sequence and head, from the walk's own first look
+    __device__ __forceinline__ Walk(const Args& args, bool report) : a(args), s0(0), at(0), todo(0), tiles(0), first(0), item(0) {
+        const int lane = threadIdx.x & 31;
+        mine = seq_info(a, lane, report);
+        int total = __reduce_add_sync(0xFFFFFFFFu, mine.tiles);
+        for (int k = 32; k < a.n_seqs; k += 32)
+            total += __reduce_add_sync(0xFFFFFFFFu, seq_info(a, k + lane, report).tiles);
+        const Shares sh(total * a.kv_heads, (int)gridDim.x);
+        begin = end = 0;
+        if ((int)blockIdx.x < sh.n) {
+            begin = sh.begin(blockIdx.x);
+            end = sh.begin(blockIdx.x + 1);
+        }
+        s.head = a.kv_heads;               // no sequence in hand
+        place();
+    }
+    __device__ __forceinline__ void place() {
+        upto = warp_sum_to(mine.tiles);
+        from = at + (upto - mine.tiles) * a.kv_heads;
+        todo = __ballot_sync(0xFFFFFFFFu, mine.tiles > 0 && from < end && from + mine.tiles * a.kv_heads > begin);
+    }
+    __device__ __forceinline__ bool next() {
+        if (s.head + 1 < a.kv_heads && item + tiles < end) {       // the next head of the sequence in hand
+            ++s.head;
+            item += tiles;
+        } else {
+            while (!todo) {
+                at += __shfl_sync(0xFFFFFFFFu, upto, 31) * a.kv_heads;
+                s0 += 32;
+                if (s0 >= a.n_seqs || at >= end) {
+                    s.n = 0;
+                    return false;
+                }
+                mine = seq_info(a, s0 + (threadIdx.x & 31), false);
+                place();
+            }
+            const int j = __ffs(todo) - 1;
+            todo &= todo - 1;
+            tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, j);
+            first = __shfl_sync(0xFFFFFFFFu, from, j);
+            s.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, j);
+            s.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, j);
+            s.seen = __shfl_sync(0xFFFFFFFFu, mine.seen, j);
+            s.seq = s0 + j;
+            s.head = begin > first ? (begin - first) / tiles : 0;
+            item = first + s.head * tiles;
+        }
+        const int t0 = max(begin - item, 0), t1 = min(end - item, tiles);
+        s.kt0 = t0;
+        s.n = t1 - t0;
+        s.part = t0 > 0 ? 0 : (t1 < tiles ? 1 : -1);
+        return true;
+    }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a) {
+    using L = Layout<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // the merge kernel may be launched now; it waits for this one's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    Ctl ctl;
+    ctl.bar0 = base + L::kBar;
+    ctl.abort = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
+    ctl.err = a.err;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMisc);
+    Seg* ring = reinterpret_cast<Seg*>(gbase + L::kSeg);
+
+    if (warp == 0 && lane < a.part_rows) {
+        // missing until written: a sum of exponentials is never negative
+        a.part_ml[(2ll * blockIdx.x) * a.part_rows + lane] = make_float2(-INFINITY, -1.0f);
+        a.part_ml[(2ll * blockIdx.x + 1) * a.part_rows + lane] = make_float2(-INFINITY, -1.0f);
+    }
+    if (threadIdx.x == 32) {
+        for (int s = 0; s < L::kSlots; ++s) {
+            ptx::mbar_init(ctl.bar(L::bFullK + s), 1);
+            ptx::mbar_init(ctl.bar(L::bEmptyK + s), 1);
+            ptx::mbar_init(ctl.bar(L::bFullV + s), 1);
+            ptx::mbar_init(ctl.bar(L::bEmptyV + s), 1);
+            ptx::mbar_init(ctl.bar(L::bLand + s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(ctl.bar(L::bQFull + s), 1);
+            ptx::mbar_init(ctl.bar(L::bQEmpty + s), 1);
+            ptx::mbar_init(ctl.bar(L::bSFull + s), 1);
+            ptx::mbar_init(ctl.bar(L::bPHalf + s), 1);
+            ptx::mbar_init(ctl.bar(L::bPFull + s), 1);
+            ptx::mbar_init(ctl.bar(L::bOFull + s), 1);
+            ptx::mbar_init(ctl.bar(L::bOEmpty + s), 1);
+        }
+        ptx::mbar_init(ctl.bar(L::bStage), 1);
+        ptx::mbar_init(ctl.bar(L::bStageFree), 1);
+        for (int s = 0; s < kSegs; ++s) {
+            ptx::mbar_init(ctl.bar(L::bSegFull + s), 1);
+            ptx::mbar_init(ctl.bar(L::bSegEmpty + s), 6);   // two producers, MMA, clearing warp, two softmax warps
+        }
+        ptx::mbar_init(ctl.bar(L::bFinal), 1);
+        *ctl.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 5 && lane == 0) {
+        ptx::prefetch_tmap(&tmQ);
+        ptx::prefetch_tmap(&tmK);
+        ptx::prefetch_tmap(&tmV);
+    }
+    // the planner and its first segment, while the others set up
+    if (warp == 4) {
+        Walk walk(a, blockIdx.x == 0);
+        bool more = walk.next();
+        if (lane == 0) ring[0] = walk.s;
+        ptx::tc_fence_before();
+        __syncthreads();
+        if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bSegFull));
+        bool ok = true;
+        for (int q = 1; ok && more; ++q) {
+            more = walk.next();
+            const int k = q % kSegs;
+            ok = ctl.warp_poll(L::bSegEmpty + k, ((q / kSegs) & 1) ^ 1);
+            if (ok && lane == 0) {
+                ring[k] = walk.s;
+                ptx::mbar_arrive(ctl.bar(L::bSegFull + k));
+            }
+            __syncwarp();
+        }
+        __syncthreads();
+        return;
+    }
+    if (warp == 2) {
+        ptx::tmem_alloc(ptx::smem_u32(tmem_slot), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = uniform(*tmem_slot);
+
+    // The q-th segment of this CTA, for one thread; false: a wait gave up.
+    auto take = [&](int q, Seg& s) -> bool {
+        if (!ctl.poll(L::bSegFull + q % kSegs, (q / kSegs) & 1)) return false;
+        s = ring[q % kSegs];
+        ptx::mbar_arrive(ctl.bar(L::bSegEmpty + q % kSegs));
+        return true;
+    };
+    // The same for a whole warp: every field the same in every lane.
+    auto warp_take = [&](int q, Seg& s) -> bool {
+        if (!ctl.warp_poll(L::bSegFull + q % kSegs, (q / kSegs) & 1)) return false;
+        const Seg r = ring[q % kSegs];
+        s.row0 = uniform(r.row0);
+        s.rows = uniform(r.rows);
+        s.seq = uniform(r.seq);
+        s.head = uniform(r.head);
+        s.seen = uniform(r.seen);
+        s.kt0 = uniform(r.kt0);
+        s.n = uniform(r.n);
+        s.part = uniform(r.part);
+        if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bSegEmpty + q % kSegs));
+        return true;
+    };
+
+    if (warp >= 5) {
+        // ------------------------------------------------------------ producers: Q and K, V
+        const bool is_v = uniform(warp) == 6;
+        if (elect_one()) {
+            Feed<HD, L::kSlots, true> feed{ctl, is_v ? &tmV : &tmK, is_v ? L::bFullV : L::bFullK,
+                                           is_v ? L::bEmptyV : L::bEmptyK, L::bLand, is_v,
+                                           base + (is_v ? L::kRingV : L::kRingK)};
+            int q = 0;
+            for (;; ++q) {
+                Seg s;
+                if (!take(q, s) || s.n == 0) break;
+                if (!is_v) {
+                    const int b = q & 1;
+                    if (q >= 2 && !ctl.poll(L::bQEmpty + b, ((q >> 1) + 1) & 1)) break;
+                    ptx::mbar_arrive_expect_tx(ctl.bar(L::bQFull + b),
+                                               (uint32_t)(a.tile_rows * a.group * 128 * L::kPanels));
+                    for (int p = 0; p < L::kPanels; ++p)
+                        ptx::tma_load_3d(base + L::kQ0 + b * L::kQ + p * kQPanel, &tmQ, ctl.bar(L::bQFull + b), p * 64,
+                                         s.head * a.group, s.row0);
+                }
+                if (!feed.tiles(a.table + (long long)s.seq * a.max_pages, a.page_shift, a.n_pages, s.kt0, s.n, s.seen,
+                                s.head)) {
+                    // Q lands before its K tiles are used, or here after a wait that gave up
+                    if (!is_v) ptx::mbar_wait(ctl.bar(L::bQFull + (q & 1)), (q >> 1) & 1, kWaitLimit);
+                    break;
+                }
+            }
+            feed.drain();
+        }
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ MMA issuer
+        if (elect_one()) {
+            constexpr uint32_t idesc_qk = ptx::idesc_bf16(BM, BN, false, false);
+            constexpr uint32_t idesc_pv = ptx::idesc_bf16(BM, HD, false, true);
+            RingPos<L::kSlots> kp, vp;
+            int steps[2] = {0, 0}, uses[2] = {0, 0};   // tiles and segments of each stream so far
+            bool ok = true;
+            for (int q = 0; ok; ++q) {
+                Seg s;
+                if (!take(q, s) || s.n == 0) break;
+                ok = ctl.poll(L::bQFull + (q & 1), (q >> 1) & 1);
+                const uint32_t qd = desc_lo(base + L::kQ0 + (q & 1) * L::kQ, 16);
+                // S0(0) S1(1) | PV(g) S(g+2) ... over the tiles g, stream g & 1
+                for (int g = -2; ok && g < s.n; g += 2) {
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        const int v = g + st, k = g + st + 2;
+                        if (v >= 0 && v < s.n) {
+                            const int j = steps[st]++;
+                            if (!ctl.poll(L::bFullV + vp.slot, vp.phase) || !ctl.poll(L::bPHalf + st, j & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            // the segment's first P V overwrites O: its last one has been read
+                            const bool fresh = v < 2;
+                            if (fresh && uses[st] > 0 && !ctl.poll(L::bOEmpty + st, (uses[st] - 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            if (fresh) ++uses[st];
+                            ptx::tc_fence_after();
+                            const uint32_t vd = desc_lo(base + L::kRingV + vp.slot * L::kTile, kPanel);
+                            const uint32_t to = tmem + tmem_o(st), tp = tmem + tmem_s(st) + kTmemP;
+#pragma unroll
+                            for (int kk = BN / 32; kk < BN / 16; ++kk)
+                                mma_ts(to, tp + kk * 8, vd + kk * 128, idesc_pv, !fresh || kk > BN / 32);
+                            if (!ctl.poll(L::bPFull + st, j & 1)) { ok = false; break; }
+                            ptx::tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < BN / 32; ++kk)
+                                mma_ts(to, tp + kk * 8, vd + kk * 128, idesc_pv, true);
+                            ptx::mma_commit(ctl.bar(L::bEmptyV + vp.slot));
+                            if (k >= s.n) ptx::mma_commit(ctl.bar(L::bOFull + st));
+                            vp.advance();
+                        }
+                        if (k < s.n) {
+                            if (!ctl.poll(L::bFullK + kp.slot, kp.phase)) { ok = false; break; }
+                            ptx::tc_fence_after();
+                            const uint32_t kd = desc_lo(base + L::kRingK + kp.slot * L::kTile, 16);
+#pragma unroll
+                            for (int kk = 0; kk < HD / 16; ++kk)
+                                mma_ss(tmem + tmem_s(st), qd - st * (kQPanel >> 4) + (((kk >> 2) * kQPanel + (kk & 3) * 32) >> 4),
+                                       kd + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), idesc_qk, kk > 0);
+                            ptx::mma_commit(ctl.bar(L::bSFull + st));
+                            ptx::mma_commit(ctl.bar(L::bEmptyK + kp.slot));
+                            if (k == s.n - 1) ptx::mma_commit(ctl.bar(L::bQEmpty + (q & 1)));
+                            kp.advance();
+                        }
+                    }
+                }
+            }
+            // all MMAs of this CTA complete before TMEM is released
+            ptx::mma_commit(ctl.bar(L::bFinal));
+            ptx::mbar_wait(ctl.bar(L::bFinal), 0, kWaitLimit);
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ V rows past the last key
+        int tiles = 0;
+        uint32_t land_phase = 0;                       // by slot: parity of its next phase
+        for (int q = 0;; ++q) {
+            Seg s;
+            if (!warp_take(q, s) || s.n == 0) break;
+            tiles += s.n;
+            const int live = s.seen - (s.kt0 + s.n - 1) * BN;
+            if (live >= BN) continue;
+            const int at = (tiles - 1) % L::kSlots;    // the segment's last V
+            if (!ctl.warp_poll(L::bLand + at, (land_phase >> at) & 1u)) break;
+            land_phase ^= 1u << at;
+            uint8_t* v = gbase + L::kRingV + at * L::kTile;
+            for (int e = live * 8 + lane; e < BN * 8; e += 32)
+                for (int p = 0; p < L::kPanels; ++p)
+                    *reinterpret_cast<uint4*>(v + p * kPanel + e * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async();               // ordered before the tensor core's reads
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bFullV + at));
+        }
+    } else {
+        // ------------------------------------------------------------ softmax of stream st
+        const int st = uniform(warp);
+        const uint32_t lane_off = (uint32_t)(st * 32) << 16;
+        const uint32_t tS = tmem + lane_off + tmem_s(st), tO = tmem + lane_off + tmem_o(st);
+        float* stage = reinterpret_cast<float*>(gbase) + lane * L::kStageRow;
+        volatile float2* stage_ml = reinterpret_cast<volatile float2*>(gbase + L::kStageMl) + lane;
+        int done_steps = 0, uses = 0;
+        for (int q = 0;; ++q) {
+            Seg s;
+            if (!warp_take(q, s) || s.n == 0) break;
+            const int steps = (s.n + 1 - st) >> 1;
+            const bool live = lane < s.rows * a.group;
+            const int first = (s.kt0 + st) * BN;
+            const int row = s.row0 + lane / a.group;
+            int limit = s.seen;
+            if (a.limits && live) limit = min(s.seen, __ldg(a.limits + row));
+            // steps whose tile every row sees whole; the rest is masked
+            const int whole = __reduce_min_sync(0xFFFFFFFFu, limit) - first - BN;
+            const int plain = whole < 0 ? 0 : min(steps, whole / (2 * BN) + 1);
+            float m = -INFINITY, l = 0.f;
+            int j = 0;
+            for (; j < steps; ++j) {
+                if (!ctl.warp_poll(L::bSFull + st, (done_steps + j) & 1)) break;
+                ptx::tc_fence_after();
+                softmax_tile<HD>(tS, j >= plain, limit - first - j * 2 * BN, a.scale_log2, m, l,
+                                 ctl.bar(L::bPHalf + st));
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + st));
+            }
+            if (j < steps) break;
+            done_steps += steps;
+            if (steps > 0) {
+                if (!ctl.warp_poll(L::bOFull + st, uses & 1)) break;
+                ++uses;
+                ptx::tc_fence_after();
+            }
+            if (st == 1) {
+                // ---- stream 1 hands its part over
+                if (q > 0 && !ctl.warp_poll(L::bStageFree, (q - 1) & 1)) break;
+                stage_ml->x = m;
+                stage_ml->y = l;
+                if (steps > 0) {
+                    uint32_t o[HD];
+                    load_row<HD>(tO, o);
+                    if (live) {
+#pragma unroll
+                        for (int v = 0; v < HD / 4; ++v)
+                            *reinterpret_cast<uint4*>(stage + 4 * v) =
+                                make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                    }
+                    ptx::tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (steps > 0) ptx::mbar_arrive(ctl.bar(L::bOEmpty + 1));
+                    ptx::mbar_arrive(ctl.bar(L::bStage));
+                }
+                continue;
+            }
+            // ---- stream 0 adds the two: out = sum w O / sum w l, w = 2^(m - M)
+            if (!ctl.warp_poll(L::bStage, q & 1)) break;
+            const float m1 = stage_ml->x, l1 = stage_ml->y;
+            const float M = fmaxf(m, m1);
+            const float w0 = l != 0.f ? ptx::ex2(m - M) : 0.f, w1 = l1 != 0.f ? ptx::ex2(m1 - M) : 0.f;
+            const float sum = w0 * l + w1 * l1;
+            const bool whole_item = s.part < 0;
+            const float scale = whole_item ? (sum != 0.f ? 1.0f / sum : 0.f) : 1.0f;
+            const float f0 = w0 * scale, f1 = w1 * scale;
+            __nv_bfloat16* orow = a.out + (long long)row * a.out_ld + (s.head * a.group + lane % a.group) * HD;
+            const long long slot = 2ll * blockIdx.x + (whole_item ? 0 : s.part);
+            float* prow = a.part_o + (slot * a.part_rows + lane) * HD;
+            uint32_t o[HD];
+            load_row<HD>(tO, o);
+            if (live) {
+                // a stream that saw no key has weight 0, and nothing in O or the stage
+#pragma unroll
+                for (int v = 0; v < HD / 4; ++v) {
+                    const float4 y = f1 != 0.f ? *reinterpret_cast<const float4*>(stage + 4 * v) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    float x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = fmaf(f1, x[e], f0 != 0.f ? f0 * __uint_as_float(o[4 * v + e]) : 0.f);
+                    if (whole_item)
+                        *reinterpret_cast<uint2*>(orow + 4 * v) =
+                            make_uint2(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]));
+                    else
+                        *reinterpret_cast<float4*>(prow + 4 * v) = make_float4(x[0], x[1], x[2], x[3]);
+                }
+            }
+            if (live && !whole_item) a.part_ml[slot * a.part_rows + lane] = make_float2(M, sum);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(ctl.bar(L::bOEmpty + 0));
+                ptx::mbar_arrive(ctl.bar(L::bStageFree));
+            }
+        }
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 2) ptx::tmem_dealloc(tmem, 512);
+}
+
+// Adds the parts of the items that shares cut.  Block b looks at the boundary
+// between CTA b and CTA b + 1 and, if it is the first one inside its item,
+// merges that item's rows, a warp per row: parts in the CTAs' order.
+template <int HD>
+__global__ void __launch_bounds__(256)
+paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
+    constexpr int E = HD / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the lists are inputs: they may be read before the attention kernel is done
+    const Shares sh(all_tiles(a, false), ctas);
+    const int c = (int)blockIdx.x + 1;
+    int row0 = 0, rows = 0, head = 0, last_cta = 0;
+    if (c < sh.n) {
+        const int cut = sh.begin(c);
+        int at = 0;
+        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+            const SeqInfo mine = seq_info(a, s0 + lane, false);
+            const int upto = warp_sum_to(mine.tiles);
+            const int next = at + __shfl_sync(0xFFFFFFFFu, upto, 31) * a.kv_heads;
+            if (cut < next) {
+                const int from = at + (upto - mine.tiles) * a.kv_heads;
+                const bool here = cut >= from && cut < from + mine.tiles * a.kv_heads;
+                const int j = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+                const int f = __shfl_sync(0xFFFFFFFFu, from, j);
+                const int tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, j);
+                head = (cut - f) / tiles;
+                const int item = f + head * tiles;
+                // the first cut inside the item, and not its beginning
+                if (cut > item && sh.begin(c - 1) <= item) {
+                    row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, j);
+                    rows = __shfl_sync(0xFFFFFFFFu, mine.rows, j);
+                    last_cta = c;
+                    while (last_cta + 1 < sh.n && sh.begin(last_cta + 1) < item + tiles) ++last_cta;
+                }
+                break;
+            }
+            at = next;
+        }
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (rows == 0) return;
+    const int parts = last_cta - c + 2;                // CTA c - 1's last part, then the first of c .. last_cta
+    auto slot_of = [&](int p) { return p == 0 ? 2ll * (c - 1) + 1 : 2ll * (c - 1 + p); };
+    for (int r = warp; r < rows * a.group; r += 8) {
+        float M = -INFINITY, acc[E], sum = 0.f;
+        bool missing = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        // one pass, relative to the largest m so far: the loads of four parts are in flight together
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) {
+            const long long at = slot_of(p) * a.part_rows + r;
+            const float2 ml = a.part_ml[at];
+            const float* src = a.part_o + at * HD + lane * E;
+            float x[E];
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(src);
+                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(src);
+                x[0] = v.x; x[1] = v.y;
+            }
+            missing = missing || ml.y < 0.f;
+            if (ml.y != 0.f) {                                 // else the part saw no key
+                const float top = fmaxf(M, ml.x);
+                const float old = M > -INFINITY ? ptx::ex2(M - top) : 0.f, w = ptx::ex2(ml.x - top);
+                sum = fmaf(w, ml.y, sum * old);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e] * old);
+                M = top;
+            }
+        }
+        if (missing) continue;                                 // JANO_ETIMEOUT was raised
+        const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+        __nv_bfloat16* dst = a.out + (long long)(row0 + r / a.group) * a.out_ld +
+                             (head * a.group + r % a.group) * HD + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(ptx::pack_bf16(acc[0] * inv, acc[1] * inv), ptx::pack_bf16(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = ptx::pack_bf16(acc[0] * inv, acc[1] * inv);
+    }
+}
+
+// Key tiles that the call's bounds allow.
+long long max_tiles(const PagedAttentionCall& c) {
+    const long long room = (long long)c.seqs->max_pages * c.pool->page_size;
+    const long long len = c.max_len < room ? c.max_len : room;
+    return ((len + BN - 1) / BN + 1) * c.seqs->n_seqs * c.pool->kv_heads;
+}
+
+template <int HD>
+cudaError_t launch_hd(const PagedAttentionCall& c, Args& a, int ctas, cudaStream_t st) {
+    using L = Layout<HD>;
+    static DeviceOnce ready;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!ready.done(dev)) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<HD>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kAlloc);
+        if (e != cudaSuccess) return e;
+        ready.mark(dev);
+    }
+    CUtensorMap mq, mk, mv;
+    if (!make_q_map(&mq, c.q, c.q_ld, c.n_rows, c.heads, HD, a.group, a.tile_rows) ||
+        !make_pool_map(&mk, c.pool->k, *c.pool) || !make_pool_map(&mv, c.pool->v, *c.pool))
+        return cudaErrorInvalidValue;
+    paged_decode_kernel<HD><<<ctas, kThreads, L::kAlloc, st>>>(mq, mk, mv, a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || ctas == 1) return e;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(ctas - 1));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_decode_merge_kernel<HD>, a, ctas);
+}
+
+}  // namespace
+
+size_t paged_decode_workspace_bytes(int max_rows, int heads, int kv_heads, int d, int sms) {
+    const long long rows = (long long)max_rows * (heads / kv_heads);
+    if (rows > kRows) return 0;
+    return (size_t)2 * sms * rows * (d + 2) * sizeof(float);
+}
+
+bool paged_decode_fits(const PagedAttentionCall& c) { return max_tiles(c) <= 0x3FFFFFFF; }
+
+cudaError_t launch_paged_decode(const PagedAttentionCall& c, int sms, int* err, cudaStream_t st) {
+    Args a{};
+    a.table = c.seqs->page_table;
+    a.lens = c.seqs->seq_lens;
+    a.cu = c.seqs->cu_rows;
+    a.limits = c.limits;
+    a.n_seqs = c.seqs->n_seqs;
+    a.max_pages = c.seqs->max_pages;
+    a.n_pages = c.pool->n_pages;
+    while ((1 << a.page_shift) < c.pool->page_size) ++a.page_shift;
+    a.n_rows = c.n_rows;
+    a.max_rows = c.max_rows;
+    const long long room = (long long)c.seqs->max_pages * c.pool->page_size;
+    a.max_len = c.max_len < room ? c.max_len : (int)room;
+    a.kv_heads = c.pool->kv_heads;
+    a.group = c.heads / c.pool->kv_heads;
+    a.tile_rows = kRows / a.group;
+    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.out = static_cast<__nv_bfloat16*>(c.out);
+    a.out_ld = c.out_ld;
+    a.part_rows = c.max_rows * a.group;
+    a.part_ml = static_cast<float2*>(c.workspace);
+    a.part_o = static_cast<float*>(c.workspace) + 4ll * sms * a.part_rows;
+    a.err = err;
+    // no more CTAs than key tiles that the bounds allow
+    const long long most = max_tiles(c);
+    const int ctas = (int)(most < sms ? most : sms);
+    return c.pool->d == 128 ? launch_hd<128>(c, a, ctas, st) : launch_hd<64>(c, a, ctas, st);
+}
+
+}  // namespace jano

@@ -39,7 +39,7 @@ def test_table_matches_fp64(J, axes, n_pos, theta, shared):
     r = J.Rope(axes=axes, n_pos=n_pos, theta=theta, shared=shared)
     got = J.rope_table(r).cpu().numpy().astype(np.float64)
     ref = op.table(axes, n_pos, theta, shared)
-    assert got.shape == ref.shape == r.table_shape
+    assert got.shape == ref.shape == (r.entries, 2)
     # cos and sin are rounded once to fp32 (2^-24 of at most 1); the angle, up
     # to 1e5, comes from a pow and a product in fp64 (a few 2^-53 of it)
     assert np.abs(got - ref).max() <= 2.0 ** -24 + 1e5 * 2.0 ** -50

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv_cache_analyzer_b200.paged as P
 import oracle.paged as op
 from paged_tools import Paged
 
@@ -26,15 +27,15 @@ odd = C.c_void_p(264)
 
 
 def cfg(J, axes=(16, 24, 24), n_pos=(2, 5, 7), grid=(5, 7), halves=0):
-    return J.jano_rope_cfg((C.c_int * 3)(*axes), (C.c_int * 3)(*n_pos), *grid, halves)
+    return bytes(J.jano_rope_cfg((C.c_int * 3)(*axes), (C.c_int * 3)(*n_pos), *grid, halves))
 
 
 def test_rope_table_refusals(J):
     L = J.lib()
-    assert J.jano_rope_table_floats(cfg(J)) == 2 * 16 + 5 * 24 + 7 * 24
+    assert L.jano_rope_table_floats(cfg(J)) == 2 * 16 + 5 * 24 + 7 * 24
     for bad in (dict(axes=(15, 24, 24)), dict(axes=(-2, 24, 24)), dict(axes=(0, 0, 0)), dict(n_pos=(0, 5, 7)),
                 dict(n_pos=(2 ** 30, 2 ** 30, 7)), dict(axes=(4, 2, 2), halves=1)):
-        assert J.jano_rope_table_floats(cfg(J, **bad)) == 0, bad
+        assert L.jano_rope_table_floats(cfg(J, **bad)) == 0, bad
         assert L.jano_rope_table(cfg(J, **bad), 10000.0, 0, fake, nil) in (EINVAL, EUNSUPPORTED), bad
     for theta in (0.0, -1.0, float("nan"), float("inf")):
         assert L.jano_rope_table(cfg(J), theta, 0, fake, nil) == EINVAL
@@ -85,13 +86,13 @@ def pool(J, **kw):
     a = dict(k=256, v=256, n_pages=9, page_size=16, kv_heads=2, d=64, page_stride=2048, token_stride=128,
              head_stride=64)
     a.update(kw)
-    return J.jano_page_pool(*a.values())
+    return bytes(J.jano_page_pool(*a.values()))
 
 
 def seqs(J, **kw):
     a = dict(page_table=256, seq_lens=256, cu_rows=256, n_seqs=3, max_pages=8)
     a.update(kw)
-    return J.jano_page_seqs(*a.values())
+    return bytes(J.jano_page_seqs(*a.values()))
 
 
 POOLS = [(dict(k=None), EINVAL), (dict(n_pages=0), EINVAL), (dict(kv_heads=0), EINVAL), (dict(page_size=8), EUNSUPPORTED),
@@ -124,49 +125,64 @@ def test_paged_append_refusals(J):
 def test_paged_attention_refusals(J):
     L = J.lib()
 
-    def call(p=None, s=None, q=fake, q_ld=256, n=8, max_rows=8, max_len=128, heads=4, scale=0.125, split=0, out=fake,
-             o_ld=256):
+    def call(p=None, s=None, q=fake, q_ld=256, n=8, max_rows=8, max_len=128, heads=4, scale=0.125, split=0, ws=nil,
+             out=fake, o_ld=256):
         return L.jano_paged_attention(p or pool(J), s or seqs(J), q, q_ld, nil, n, max_rows, max_len, heads, scale, split,
-                                      out, o_ld, nil)
+                                      ws, 0, out, o_ld, nil)
     assert call(n=0, q=nil) == 0 and call(n=-1) == EINVAL and call(max_len=-1) == EINVAL and call(max_rows=-1) == EINVAL
     for kw, code in POOLS:
         assert call(p=pool(J, **kw)) == code, kw
     for kw, code in SEQS:
         assert call(s=seqs(J, **kw)) == code, kw
-    for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(split=3), dict(split=32),
+    for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(split=3), dict(split=16),
                dict(split=-1), dict(q=nil), dict(out=nil), dict(heads=0)):
         assert call(**kw) == EINVAL, kw
     assert call(heads=3, q_ld=192, o_ld=192) == ESHAPE                    # not a multiple of the K/V heads
     assert call(heads=258, q_ld=258 * 64, o_ld=258 * 64) == EUNSUPPORTED  # 129 query heads per K/V head
     assert call(p=pool(J, d=96, token_stride=192, head_stride=96), q_ld=384, o_ld=384) == EUNSUPPORTED
     assert call(q_ld=128) == ESHAPE and call(o_ld=260) == EUNSUPPORTED and call(q=odd) == EALIGN
+    assert call(ws=odd) == EALIGN
 
 
 def test_split_choice_is_host_only(J):
     f = J.jano_paged_attention_splits_on
     assert f(75600, 75600, 75600, 1, 40, 40, 148) == 1            # enough query tiles to fill the SMs
     assert f(1, 1, 128, 1, 24, 24, 148) == 1                      # one key tile
-    assert f(1, 1, 75600, 1, 8, 8, 148) == 16                     # eight heads, 591 key tiles
+    assert f(1, 1, 75600, 1, 8, 8, 148) == 8                      # eight heads, 591 key tiles
+    # the best of the measured splits: 12 heads over 32,760 keys, 4 heads over 8,192
+    assert [f(n, n, 32760, 1, 12, 12, 148) for n in (1638, 3276, 4680, 16380)] == [4, 4, 4, 2]
+    assert f(1000, 1000, 8192, 1, 4, 4, 148) == 4 and f(4 * 256, 256, 2048, 4, 12, 12, 148) == 2
     assert f(0, 1, 128, 1, 4, 4, 148) == 1 and f(1, 1, 128, 1, 4, 3, 148) == 1 and f(1, 1, 128, 1, 129, 1, 148) == 1
     for n in (1, 33, 1000):
         for length in (1, 200, 5000, 75600):
             for kv in (1, 8, 40):
                 z = f(n, n, length, 1, kv, kv, 148)
-                assert z in (1, 2, 4, 8, 16) and (z == 1 or -(-length // 128) >= 2 * z)
+                assert z in (1, 2, 4, 8) and z <= -(-length // 128)
 
 
 def test_python_refusals_need_no_gpu(J):
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     r = J.Rope(axes=(16, 24, 24), n_pos=(2, 5, 7), grid=(5, 7))
-    table = torch.zeros(*r.table_shape)
+    table = torch.zeros(r.entries, 2)
     with pytest.raises(ValueError, match="CUDA tensor"):
         J.axis_rope(x, r, table)
-    with pytest.raises(TypeError, match="bfloat16"):
-        J.axis_rope(x.float(), r, table)
     with pytest.raises(ValueError, match=r"\[rows\]\[heads\]\[d\]"):
         J.axis_rope(x[0], r, table)
+    rows = lambda t, n=4, h=2, d=64: P._rows(t, "x", -1, n, h, d)         # as on device -1
+    with pytest.raises(TypeError, match="bfloat16"):
+        rows(x.float())
     with pytest.raises(ValueError, match="adjacent"):
-        J.axis_rope(x.transpose(1, 2), r, table)
+        rows(x.transpose(1, 2), h=64, d=2)
+    with pytest.raises(ValueError, match=r"\[4\]\[3\]\[64\]"):
+        rows(x, h=3)
+    with pytest.raises(TypeError, match="int32"):
+        P._list(torch.zeros(4), "ids", 4, -1)
+    with pytest.raises(ValueError, match="5 elements"):
+        P._list(torch.zeros(4, dtype=torch.int32), "ids", 5, -1)
+    with pytest.raises(ValueError, match="contiguous"):
+        P._list(torch.zeros(8, dtype=torch.int32)[::2], "ids", 4, -1)
+    with pytest.raises(ValueError, match="cuda:3"):                       # another device than the first tensor's
+        P._list(torch.zeros(4, dtype=torch.int32), "ids", 4, 3)
     with pytest.raises(ValueError, match="pairing"):
         J.Rope(axes=(16, 24, 24), n_pos=(2, 5, 7), pairing="quarters")
     with pytest.raises(ValueError, match="three entries"):
@@ -178,20 +194,27 @@ def test_python_refusals_need_no_gpu(J):
     with pytest.raises(ValueError, match="CUDA tensor"):
         J.paged_append(p.q, p.q, ints([0, 1, 2, 3]), p.k, p.v, ints(p.table), ints(p.lens), ints(p.cu))
     with pytest.raises(ValueError, match="same strides"):
-        J._pool(p.k, p.v.transpose(1, 2).contiguous().transpose(1, 2))
+        P._pool(p.k, p.v.transpose(1, 2).contiguous().transpose(1, 2), -1)
+    with pytest.raises(TypeError, match="v_pages must be torch.bfloat16"):
+        P._pool(p.k, p.v.float(), -1)
 
 
 def test_size_one_dimensions_take_any_stride(J):
     # a pool of one page or one K/V head: torch reports whatever stride made the view
     k = torch.zeros(5, 32, 1, 64, dtype=torch.bfloat16)[:1]
-    c = J._pool(k.as_strided(k.shape, (7, 64, 3, 1)), k.as_strided(k.shape, (7, 64, 3, 1)))
+    k = k.as_strided(k.shape, (7, 64, 3, 1))
+    c = J.jano_page_pool.from_buffer_copy(P._pool(k, k, -1))
     assert (c.page_stride, c.token_stride, c.head_stride) == (32 * 64, 64, 64)
-    assert J._rows(k[0, :1], "x") == 64 and J._rows(torch.zeros(3, 9, 64, dtype=torch.bfloat16)[:, 2:3], "x") == 576
+    assert (c.k, c.n_pages, c.page_size, c.kv_heads, c.d) == (k.data_ptr(), 1, 32, 1, 64)
+    wide = torch.zeros(3, 9, 64, dtype=torch.bfloat16)[:, 2:3]
+    assert P._rows(wide[:1], "x", -1, 1, 1, 64)[1] == 64 and P._rows(wide, "x", -1, 3, 1, 64)[1] == 576
 
 
 def test_rope_of_a_geometry(J):
     r = J.Rope.of(J.Geometry(21, 60, 104), (44, 42, 42))
-    assert r.n_pos == (21, 30, 52) and r.grid == (30, 52) and r.table_shape == (21 * 22 + 30 * 21 + 52 * 21, 2)
+    assert r.n_pos == (21, 30, 52) and r.grid == (30, 52) and r.entries == 21 * 22 + 30 * 21 + 52 * 21
+    c = r.c()
+    assert (list(c.axes), list(c.n_pos), c.grid_h, c.grid_w, c.halves) == ([44, 42, 42], [21, 30, 52], 30, 52, 0)
 
 
 # ------------------------------------------------------------------ oracle pins
