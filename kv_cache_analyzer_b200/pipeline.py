@@ -8,6 +8,7 @@ sampling step of the method:
   a2  jano_classify         per-token field     -> token levels (Static/Moderate/Active)
   a3  jano_build_schedule   token levels        -> per-step due lists (CSR)
   a4  jano_kv_scatter       fresh K/V of the due tokens -> persistent cache
+      (jano_rope_scatter with a rope: K and the queries rotated on the way)
   a5  jano_active_attention due queries over the whole cache -> out[idx]
       (jano_active_attention_split for due sets too small to fill the GPU)
 
@@ -24,6 +25,7 @@ import torch
 from . import (Geometry, Schedule, SplitWorkspace, attention_auto, jano_block_scores,
                jano_build_schedule, jano_build_schedule_workspace_bytes,
                jano_classify, jano_kv_scatter)
+from .paged import Rope, rope_scatter, rope_table
 
 KERNELS_PER_STEP = 6      # scores 1 + classify 1 + schedule 2 + scatter 1 + attention 1
                           # (attention 2 when its keys are split: + the merge pass)
@@ -33,7 +35,7 @@ class HotPath:
     def __init__(self, *, K: int, C: int, latent_geom: Geometry, token_geom: Geometry,
                  heads: int, d: int, frac_active: float, frac_static: float,
                  sched: Schedule, device="cuda", stream: torch.cuda.Stream | None = None,
-                 w_temporal: float = 0.5, w_spatial: float = 0.5):
+                 w_temporal: float = 0.5, w_spatial: float = 0.5, rope: Rope | None = None):
         self.K, self.C, self.heads, self.d = K, C, heads, d
         self.lg, self.tg, self.sched = latent_geom, token_geom, sched
         self.frac_active, self.frac_static = frac_active, frac_static
@@ -58,7 +60,10 @@ class HotPath:
         self.out = torch.zeros((N, heads, d), dtype=torch.bfloat16, **e)
         self.att_ws = SplitWorkspace(self.dev)   # key-split attention workspace
         self.last_split = 1
-        self.q_act = self.k_act = self.v_act = None
+        self.q_act = self.k_act = self.v_act = self.q_rot = None
+        # with a rope, q_act and k_act hold the unrotated rows and stay as they are
+        self.rope = rope
+        self.rope_table = None if rope is None else rope_table(rope, stream=self.stream)
         self.host_offsets = None
         self._lgc, self._tgc, self._sc = lg.c(), token_geom.c(), sched.c()
 
@@ -69,6 +74,7 @@ class HotPath:
         self.q_act = torch.empty(shape, **e)
         self.k_act = torch.empty(shape, **e)
         self.v_act = torch.empty(shape, **e)
+        self.q_rot = None if self.rope is None else torch.empty(shape, **e)
 
     def run_plan_kernels(self, events=None):
         """a1..a3 on the stream (no host synchronisation)."""
@@ -111,10 +117,15 @@ class HotPath:
         self.run_plan_kernels(ev[:4])
         start, n_act = self.due(step)
         idx = self.idx[start:start + n_act]
-        jano_kv_scatter(self.k_act, self.v_act, idx, n_act, self.heads, self.d,
-                        self.k_cache, self.v_cache, self.N, s)
+        q = self.q_act
+        if self.rope is None:
+            jano_kv_scatter(self.k_act, self.v_act, idx, n_act, self.heads, self.d,
+                            self.k_cache, self.v_cache, self.N, s)
+        else:
+            q = rope_scatter(self.k_act[:n_act], self.v_act[:n_act], idx, self.k_cache, self.v_cache, self.rope,
+                             self.rope_table, q=self.q_act[:n_act], q_out=self.q_rot[:n_act], stream=s)
         if ev[4] is not None: ev[4].record(s)
-        self.last_split = attention_auto(self.q_act, self.k_cache, self.v_cache, idx, n_act, self.N,
+        self.last_split = attention_auto(q, self.k_cache, self.v_cache, idx, n_act, self.N,
                                          self.heads, self.d, self.out, s, self.att_ws)
         if ev[5] is not None: ev[5].record(s)
         return n_act

@@ -26,6 +26,7 @@ import torch
 from . import (Geometry, Schedule, SplitWorkspace, attention_auto, jano_block_scores,
                jano_build_schedule, jano_build_schedule_workspace_bytes, jano_classify,
                jano_kv_scatter)
+from .paged import Rope, rope_scatter, rope_table
 
 
 def head_range(rank: int, world: int, heads: int) -> tuple[int, int]:
@@ -75,14 +76,15 @@ class ShardedHotPath:
     Buffers: `lat` is the rank's latent slab [K+1][C][F_slab][H][W];
     `q_act`, `k_act`, `v_act` [n_cap][H_r][d] and `k_cache`, `v_cache`, `out`
     [N][H_r][d] hold the rank's heads; `scores` [n_blocks] all ranks' block
-    scores after the gather."""
+    scores after the gather.  With a rope, q_act and k_act hold unrotated rows,
+    turned on the way into the cache (by token, so alike on every rank)."""
 
     def __init__(self, *, rank: int, world: int, K: int, C: int, latent_geom: Geometry,
                  token_geom: Geometry, heads: int, d: int, frac_active: float,
                  frac_static: float, sched: Schedule, device="cuda",
                  stream: Optional[torch.cuda.Stream] = None,
                  all_gather: Callable = torch_all_gather,
-                 w_temporal: float = 0.5, w_spatial: float = 0.5):
+                 w_temporal: float = 0.5, w_spatial: float = 0.5, rope: Optional[Rope] = None):
         self.rank, self.world = rank, world
         self.K, self.C, self.d = K, C, d
         self.lg, self.tg, self.sched = latent_geom, token_geom, sched
@@ -121,7 +123,9 @@ class ShardedHotPath:
         self.out = torch.zeros(shape, dtype=torch.bfloat16, **e)
         self.att_ws = SplitWorkspace(self.dev)   # key-split attention workspace
         self.last_split = 1
-        self.q_act = self.k_act = self.v_act = None
+        self.q_act = self.k_act = self.v_act = self.q_rot = None
+        self.rope = rope
+        self.rope_table = None if rope is None else rope_table(rope, stream=self.stream)
         self.host_offsets = None
         self._sgc, self._tgc, self._sc = self.slab_geom.c(), token_geom.c(), sched.c()
 
@@ -130,6 +134,7 @@ class ShardedHotPath:
         e = dict(device=self.dev, dtype=torch.bfloat16)
         shape = (n_act_cap, self.heads, self.d)
         self.q_act, self.k_act, self.v_act = (torch.empty(shape, **e) for _ in range(3))
+        self.q_rot = None if self.rope is None else torch.empty(shape, **e)
 
     def load_latent(self, lat_full: torch.Tensor):
         """This rank's frames (and the halo frame) of the full latent history."""
@@ -184,10 +189,15 @@ class ShardedHotPath:
         if self.heads == 0:
             return n_act
         idx = self.idx[start:start + n_act]
-        jano_kv_scatter(self.k_act, self.v_act, idx, n_act, self.heads, self.d,
-                        self.k_cache, self.v_cache, self.N, s)
+        q = self.q_act
+        if self.rope is None:
+            jano_kv_scatter(self.k_act, self.v_act, idx, n_act, self.heads, self.d,
+                            self.k_cache, self.v_cache, self.N, s)
+        else:
+            q = rope_scatter(self.k_act[:n_act], self.v_act[:n_act], idx, self.k_cache, self.v_cache, self.rope,
+                             self.rope_table, q=self.q_act[:n_act], q_out=self.q_rot[:n_act], stream=s)
         # a rank's few heads give few CTAs: the keys are split when that fills the SMs better
-        self.last_split = attention_auto(self.q_act, self.k_cache, self.v_cache, idx, n_act, self.N,
+        self.last_split = attention_auto(q, self.k_cache, self.v_cache, idx, n_act, self.N,
                                          self.heads, self.d, self.out, s, self.att_ws)
         return n_act
 

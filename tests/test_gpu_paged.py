@@ -193,6 +193,99 @@ def test_attention_matches_oracle(J, rows, lens, heads, kv_heads, d, page, kind,
     assert bool((out[int(p.cu[-1]):] == 3.0).all())               # rows behind the last sequence
 
 
+FEW = [  # at most 32 packed rows per sequence: the form in which every SM takes an equal share of the key tiles
+    ([1], [1], 1, 1, 64, 16, None, {}),
+    ([1], [128], 1, 1, 128, 128, None, {}),
+    ([1], [129], 3, 3, 128, 16, None, {}),
+    ([1], [5000], 2, 2, 64, 64, None, {}),                             # two items cut over some twenty CTAs each
+    ([1, 1, 1], [700, 128, 1], 8, 2, 128, 16, None, {}),
+    ([2, 0, 2, 1], [130, 50, 31, 2000], 10, 1, 64, 32, "token", {}),   # 20 of 32 rows, one sequence without any
+    ([1, 1], [3, 300], 32, 1, 128, 256, None, {}),
+    ([32, 5, 17], [257, 383, 40], 2, 2, 128, 64, "random", {}),
+    ([8, 8], [600, 90], 12, 3, 64, 16, "random", dict(head_major=True)),
+    ([1] * 70, [(s * 97) % 400 + 1 for s in range(70)], 4, 2, 64, 16, None, dict(pad_rows=3)),   # three looks of 32
+    ([1] * 40, [1] * 40, 2, 2, 128, 16, None, {}),                     # fewer tiles than SMs
+    ([2, 1, 1], [0, 0, 5], 2, 2, 64, 16, None, dict(one_buffer=True, pad_rows=2)),
+    ([3, 3], [300, 200], 6, 2, 128, 32, "dark", {}),                   # a sequence whose rows all see nothing
+]
+
+
+@pytest.mark.parametrize("rows,lens,heads,kv_heads,d,page,kind,opt", FEW)
+def test_few_rows_match_oracle(J, rows, lens, heads, kv_heads, d, page, kind, opt):
+    p = Paged(rows, lens, heads, kv_heads, d, page, seed=sum(lens), **opt)
+    n = int(p.cu[-1])
+    limits = limits_of(None if kind == "dark" else kind, rows, lens)
+    if kind == "dark":
+        limits = np.array([5, 300, 77, 0, -4, 0])
+    if limits is not None and opt.get("pad_rows"):
+        limits = np.concatenate([limits, np.zeros(opt["pad_rows"], dtype=limits.dtype)])
+    need = J.jano_paged_attention_workspace_bytes(max(rows), heads, kv_heads, d)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert need == 2 * sms * max(rows) * heads // kv_heads * (d + 2) * 4
+    # garbage in the workspace, as a reused buffer would hold
+    ws = torch.full((need // 4,), float("nan"), dtype=torch.float32, device="cuda").view(torch.uint8)
+    outs = []
+    for kw in (dict(workspace=ws), dict(workspace=ws, max_len=max(max(lens), 1)), {}):
+        out = torch.full_like(p.dev_q, 3.0)
+        attend(J, p, limits, out=out, max_rows=max(rows), **kw)
+        no_device_error(J)
+        p.check(out, limits)
+        assert bool((out[n:] == 3.0).all())
+        outs.append(out)
+    assert all(torch.equal(o, outs[0]) for o in outs)             # the same sums in the same order
+
+
+def test_few_rows_report_bad_lists_and_need_their_workspace(J):
+    p = Paged([1, 2], [100, 200], 2, 2, 64, 16, seed=12)
+    out = torch.full_like(p.dev_q, 3.0)
+    want = attend(J, p, max_rows=2).clone()
+    for kw, dark in ((dict(lens=[100, -1]), slice(1, 3)), (dict(lens=[10 ** 9, 200]), slice(0, 1)),
+                     (dict(cu=[0, 1, 4]), slice(1, 3)), (dict(cu=[2, 3, 3]), slice(0, 2))):
+        out.fill_(3.0)
+        J.paged_attention(p.dev_q, p.dev_k, p.dev_v, p.dev_table, ints(kw["lens"]) if "lens" in kw else p.dev_lens,
+                          ints(kw["cu"]) if "cu" in kw else p.dev_cu, out=out, max_rows=2)
+        assert J.device_error() == 6, kw
+        assert bool((out[dark] == 3.0).all()), kw
+    table = p.table.copy()
+    table[0, 2] = p.n_pages
+    J.paged_attention(p.dev_q, p.dev_k, p.dev_v, ints(table), p.dev_lens, p.dev_cu, out=out, max_rows=2)
+    assert J.device_error() == 6
+    assert torch.equal(out[1:], want[1:]) and torch.isfinite(out.float()).all()
+    with pytest.raises(J.JanoError, match="EINVAL"):
+        attend(J, p, max_rows=2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(TypeError, match="uint8"):
+        attend(J, p, max_rows=2, workspace=torch.empty(10 ** 6, device="cuda"))
+    no_device_error(J)
+
+
+def test_few_rows_calls_at_once_on_streams_and_replayed(J):
+    cases = [Paged([1, 1, 1], [1500 + 300 * i, 77, 900], 4, 2, 128, 32, seed=20 + i) for i in range(4)]
+    want = [attend(J, p, max_rows=1).clone() for p in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[attend(J, p, max_rows=1, stream=s) for p, s in zip(cases, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for r in outs for o, w in zip(r, want))
+    # two graphs, captured one after the other, replayed together
+    graphs, res = [], []
+    for p, s in zip(cases[:2], streams):
+        o = torch.zeros_like(p.dev_q)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                attend(J, p, max_rows=1, out=o)
+        graphs.append(g)
+        res.append(o)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    no_device_error(J)
+    assert torch.equal(res[0], want[0]) and torch.equal(res[1], want[1])
+    del graphs, g
+
+
 def test_attention_takes_strided_rows_and_bounds(J):
     p = Paged([33, 70], [210, 333], 4, 2, 64, 32, seed=8)
     wide = torch.zeros(p.n, 3 * 4, 64, dtype=torch.bfloat16, device="cuda")

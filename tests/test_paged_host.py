@@ -217,6 +217,49 @@ def test_rope_of_a_geometry(J):
     assert (list(c.axes), list(c.n_pos), c.grid_h, c.grid_w, c.halves) == ([44, 42, 42], [21, 30, 52], 30, 52, 0)
 
 
+# ------------------------------------------------------------------ page bookkeeping
+def test_pages_are_handed_out_returned_and_never_shared():
+    from kv_cache_analyzer_b200.serving import PagedBatch
+    b = PagedBatch(n_pages=10, page_size=16, heads=4, kv_heads=2, d=64, device="cpu")
+    a, c = b.open(33), b.open(64)                                  # 3 and 4 pages
+    assert b.free_pages == 3 and b.k_pages.shape == (10, 16, 2, 64)
+    with pytest.raises(RuntimeError, match="exhausted: 4 pages needed, 3 free"):
+        b.open(50)
+    assert b.free_pages == 3
+    b.extend(a, 48)                                                # still 3 pages
+    b.extend(a, 49)
+    assert b.free_pages == 2
+    with pytest.raises(RuntimeError, match="exhausted"):
+        b.extend(a, 200)
+    with pytest.raises(ValueError, match="cannot shrink"):
+        b.extend(a, 10)
+    p = b.plan([(c, 5), (a, 1)])
+    t = p.lists["page_table"]
+    assert t.shape == (2, 4) and len(set(t.flatten().tolist())) == 8
+    assert p.lists["seq_lens"].tolist() == [64, 49] and p.lists["cu_rows"].tolist() == [0, 5, 6]
+    assert (p.max_rows, p.max_len, p.n_rows) == (5, 64, 6)
+    with pytest.raises(ValueError, match="once"):
+        b.plan([(a, 1), (a, 2)])
+    with pytest.raises(ValueError, match="at least one"):
+        b.plan([])
+    with pytest.raises(ValueError, match="negative"):
+        b.plan([(a, -1)])
+    rows = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="plan has 6 rows, got 5"):
+        b.step(p, rows, rows[:, :2], rows[:, :2], torch.zeros(5, dtype=torch.int32))
+    b.close(a)
+    with pytest.raises(ValueError, match="grew or closed"):
+        b.step(p, rows, rows[:, :2], rows[:, :2], torch.zeros(6, dtype=torch.int32))
+    p = b.plan([(c, 1)])
+    b.extend(c, 65)
+    with pytest.raises(ValueError, match="grew or closed"):
+        b.step(p, rows, rows[:, :2], rows[:, :2], torch.zeros(1, dtype=torch.int32))
+    assert b.free_pages == 5
+    d = b.open(80)
+    t = b.plan([(c, 1), (d, 1)]).lists["page_table"]
+    assert t.shape == (2, 5) and len(set(t.flatten().tolist())) == 10
+
+
 # ------------------------------------------------------------------ oracle pins
 def test_oracle_rope_by_hand():
     # one head of 8 columns, axes of 2, 2 and 4: slots at 1, 1, 1 and theta^-1/2 = 1/100
