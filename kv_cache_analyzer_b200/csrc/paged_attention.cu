@@ -336,9 +336,9 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                                          row0 + a.tile_rows);
                 }
             }
-            Feed<HD, L::kSlots, false> feed{ctl, is_v ? &tmV : &tmK, is_v ? L::bFullV : L::bFullK,
+            Feed<HD, false> feed{ctl, is_v ? &tmV : &tmK, is_v ? L::bFullV : L::bFullK,
                                             is_v ? L::bEmptyV : L::bEmptyK, L::bLand, is_v,
-                                            base + (is_v ? L::kRingV : L::kRingK)};
+                                            base + (is_v ? L::kRingV : L::kRingK), RingPos(L::kSlots)};
             feed.tiles(a.table + (long long)seq * a.max_pages, a.page_shift, a.n_pages, kt0, n, seen, head);
             if (!is_v) ptx::mbar_wait(ctl.bar(L::bQFull), 0, kWaitLimit);
             feed.drain();
@@ -348,7 +348,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         if (elect_one()) {
             constexpr uint32_t idesc_qk = ptx::idesc_bf16(BM, BN, false, false);
             constexpr uint32_t idesc_pv = ptx::idesc_bf16(BM, HD, false, true);
-            RingPos<L::kSlots> kp, vp;
+            RingPos kp(L::kSlots), vp(L::kSlots);
             auto wait_k = [&]() { return ctl.poll(L::bFullK + kp.slot, kp.phase); };
             auto wait_v = [&]() { return ctl.poll(L::bFullV + vp.slot, vp.phase); };
             auto release_k = [&]() { ptx::mma_commit(ctl.bar(L::bEmptyK + kp.slot)); kp.advance(); };

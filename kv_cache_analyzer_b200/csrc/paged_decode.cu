@@ -9,19 +9,29 @@
 // sequence's head, the CTA leaves a partial (O, m, l) and a second kernel, its
 // programmatic dependent, adds the parts in order.  Within a CTA the loads of
 // the next (sequence, head) start while the last one is still being worked
-// on: all barriers count through, Q has two buffers, and as a tile of 32 live
-// rows needs only 8 KB of Q, six K/V tiles of 32 KB (d = 128) fit beside it
-// (four in paged_attention.cu).  The MMAs have M = 128 all the same; the rows
-// past 32 read whatever shared memory follows, and nobody reads their results.
+// on: all barriers count through, and Q has two buffers.
+//
+// 128 KB of K/V tiles per SM: with 96 KB one token each of 32 sequences
+// (d = 128, 2.8 GB of K/V) took 471 us, with 128 or 160 KB 405, with 192 KB
+// 434, as the SMs then finish further apart (340 to 435 us).
+//
+// Reading 7 TB/s takes the card to its power limit by itself, so the tensor
+// core's share of the power costs time, though its time does not: the MMAs
+// have the smallest M that holds the rows (64 for 16 packed rows, 128 for 32),
+// and their other rows are zeros, kept around Q.  The same 32 sequences over
+// and over, at 1000 W: 480 us with M = 128 over whatever lay behind Q (SM clock
+// 1,080 MHz), 448 with zeros there (1,300), 424 with M = 64 (1,540); a plain
+// sum of as many bytes takes 408 (1,680).  Cold, 405 us: 6.9 TB/s.
 //
 // 7 warps:  0, 1  softmax of streams 0 and 1 (even and odd key tiles; thread =
-// packed row.  Stream 1's operand starts 32 rows before Q, so its rows fall
-// into the TMEM lanes that warp 1 reaches, on another scheduler), 2 MMA
-// issuer, 3 clears V rows past the visible length, 4 planner: it walks the
-// device's lists once and hands the CTA's segments (runs of key tiles of one
-// sequence and head) to the others through a small ring, 5 producer of Q and
-// K, 6 producer of V.  The two streams' parts are joined through shared memory
-// at the end of each segment.
+// packed row.  Stream 1's operand starts R rows before Q, so its rows fall
+// into the TMEM lanes that warp 1 reaches, on another scheduler; with M = 64
+// every quarter of the lanes holds 16 rows), 2 MMA issuer, 3 clears V rows past
+// the visible length, 4 planner: it walks the device's lists once and hands
+// the CTA's segments (runs of key tiles of one sequence and head) to the
+// others through a small ring, 5 producer of Q and K, 6 producer of V.  The
+// two streams' parts are joined through shared memory at the end of each
+// segment.
 //
 // Every wait is bounded.  The partial slots of a CTA are marked missing before
 // it starts, so that rows of a CTA that gave up are not written.
@@ -31,9 +41,8 @@ namespace jano {
 namespace {
 
 constexpr int kThreads = 224;                // two warps per scheduler at most: 255 registers for a thread's S row
-constexpr int kRows = 32;                    // packed rows at most
+constexpr int kMaxRows = 32;                 // packed rows at most
 constexpr int kSegs = 4;                     // segments in the planner's ring
-constexpr uint32_t kQPanel = kRows * 128;    // bytes of one 32-row x 64-column panel
 
 // A run of key tiles of one (sequence, K/V head).
 struct Seg {
@@ -44,27 +53,32 @@ struct Seg {
     int part;            // partial slot of the CTA that it goes to; -1: the whole item, straight to out
 };
 
-template <int HD>
+// R: packed rows of the form (16 or 32), a quarter of its MMAs' M.
+template <int HD, int R>
 struct Layout {
+    static constexpr int kM = 4 * R;
     static constexpr int kPanels = HD / 64;
-    static constexpr int kSlots = HD == 64 ? 6 : 3;               // K tiles, and V tiles: 192 KB together
     static constexpr uint32_t kTile = kPanels * kPanel;
+    static constexpr uint32_t kQRows = R * 128;                   // bytes of the R rows of one 64-column panel
+    static constexpr uint32_t kQPanel = kM * 128;                 // ... and of the zeros that follow
     static constexpr uint32_t kQ = kPanels * kQPanel;             // one Q buffer
-    // stream 1's O, float [kRows][kStageRow] (padded: adjacent rows on different
-    // banks), its (m, l), then Q and the ring: an MMA of stream 1 reads 4 KB
-    // before a Q panel and either one up to 16 KB past its start
+    // stream 1's O, float [R][kStageRow] (padded: adjacent rows on different
+    // banks), its (m, l), then R rows of zeros (stream 1's operand starts
+    // there) and the two Q buffers
     static constexpr uint32_t kStageRow = HD + 4;
-    static constexpr uint32_t kStageMl = kRows * kStageRow * 4;
-    static constexpr uint32_t kQ0 = (kStageMl + kRows * 8 + 1023) / 1024 * 1024;
+    static constexpr uint32_t kStageMl = R * kStageRow * 4;
+    static constexpr uint32_t kZeros = (kStageMl + 32 * 8 + 1023) / 1024 * 1024;
+    static constexpr uint32_t kQ0 = kZeros + kQRows;
     static constexpr uint32_t kRingK = kQ0 + 2 * kQ;
+    static constexpr int kSlots = 128 * 1024 / kTile / 2;         // K tiles, and V tiles, see above
     static constexpr uint32_t kRingV = kRingK + kSlots * kTile;
     static constexpr uint32_t kBar = kRingV + kSlots * kTile;
     static constexpr int bFullK = 0;                   // [kSlots]
-    static constexpr int bEmptyK = bFullK + kSlots;    // [kSlots]
-    static constexpr int bFullV = bEmptyK + kSlots;    // [kSlots] landed and cleared past the last key
-    static constexpr int bEmptyV = bFullV + kSlots;    // [kSlots]
-    static constexpr int bLand = bEmptyV + kSlots;     // [kSlots] a ragged V tile landed, not yet cleared
-    static constexpr int bQFull = bLand + kSlots;      // [2]
+    static constexpr int bEmptyK = bFullK + kSlots;   // [kSlots]
+    static constexpr int bFullV = bEmptyK + kSlots;   // [kSlots] landed and cleared past the last key
+    static constexpr int bEmptyV = bFullV + kSlots;   // [kSlots]
+    static constexpr int bLand = bEmptyV + kSlots;    // [kSlots] a ragged V tile landed, not yet cleared
+    static constexpr int bQFull = bLand + kSlots;     // [2]
     static constexpr int bQEmpty = bQFull + 2;         // [2]
     static constexpr int bSFull = bQEmpty + 2;         // [2]
     static constexpr int bPHalf = bSFull + 2;          // [2]
@@ -73,7 +87,8 @@ struct Layout {
     static constexpr int bOEmpty = bOFull + 2;         // [2]
     static constexpr int bStage = bOEmpty + 2;
     static constexpr int bStageFree = bStage + 1;
-    static constexpr int bSegFull = bStageFree + 1;    // [kSegs]
+    static constexpr int bZeros = bStageFree + 1;      // the rows around Q are cleared
+    static constexpr int bSegFull = bZeros + 1;        // [kSegs]
     static constexpr int bSegEmpty = bSegFull + kSegs; // [kSegs]
     static constexpr int bFinal = bSegEmpty + kSegs;
     static constexpr int kNumBars = bFinal + 1;
@@ -82,7 +97,7 @@ struct Layout {
     static constexpr uint32_t kBytes = kMisc + 16;                // tmem base, abort flag, share is empty
     static constexpr uint32_t kAlloc = kBytes + 1024;             // slack for 1 KB alignment
     static_assert(kAlloc <= 227 * 1024, "shared memory budget");
-    static_assert(kQ0 >= kQPanel && kRingK % 1024 == 0 && kBar % 8 == 0, "alignment");
+    static_assert(kQ0 % 1024 == 0 && kRingK % 1024 == 0 && kBar % 8 == 0, "alignment");
 };
 
 struct Args {
@@ -156,6 +171,10 @@ struct Shares {
     int n, each, more;
     __device__ Shares(int total, int ctas) : n(max(1, min((total + 1) / 2, ctas))), each(total / n), more(total - each * n) {}
     __device__ int begin(int c) const { return c * each + min(c, more); }
+    __device__ int owner(int tile) const {         // the share that a tile lies in
+        const int long_ones = more * (each + 1);
+        return tile < long_ones ? tile / (each + 1) : more + (tile - long_ones) / each;
+    }
 };
 
 // The segments of one CTA's share, one after another (a whole warp walks).
@@ -224,11 +243,11 @@ struct Walk {
     }
 };
 
-template <int HD>
+template <int HD, int R>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args a) {
-    using L = Layout<HD>;
+    using L = Layout<HD, R>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -269,6 +288,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         }
         ptx::mbar_init(ctl.bar(L::bStage), 1);
         ptx::mbar_init(ctl.bar(L::bStageFree), 1);
+        ptx::mbar_init(ctl.bar(L::bZeros), 3);
         for (int s = 0; s < kSegs; ++s) {
             ptx::mbar_init(ctl.bar(L::bSegFull + s), 1);
             ptx::mbar_init(ctl.bar(L::bSegEmpty + s), 6);   // two producers, MMA, clearing warp, two softmax warps
@@ -313,6 +333,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     ptx::tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
 
+    // the rows around Q, while the first tiles are on their way (warps 0, 1, 3)
+    auto clear_around_q = [&] {
+        const int at = (warp == 3 ? 2 : warp) * 32 + lane;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (uint32_t e = at * 16; e < L::kQRows; e += 96 * 16) *reinterpret_cast<uint4*>(gbase + L::kZeros + e) = zero;
+        for (int p = 0; p < 2 * L::kPanels; ++p)
+            for (uint32_t e = L::kQRows + at * 16; e < L::kQPanel; e += 96 * 16)
+                *reinterpret_cast<uint4*>(gbase + L::kQ0 + p * L::kQPanel + e) = zero;
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bZeros));
+    };
+
     // The q-th segment of this CTA, for one thread; false: a wait gave up.
     auto take = [&](int q, Seg& s) -> bool {
         if (!ctl.poll(L::bSegFull + q % kSegs, (q / kSegs) & 1)) return false;
@@ -340,9 +373,10 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         // ------------------------------------------------------------ producers: Q and K, V
         const bool is_v = uniform(warp) == 6;
         if (elect_one()) {
-            Feed<HD, L::kSlots, true> feed{ctl, is_v ? &tmV : &tmK, is_v ? L::bFullV : L::bFullK,
+            Feed<HD, true> feed{ctl, is_v ? &tmV : &tmK, is_v ? L::bFullV : L::bFullK,
                                            is_v ? L::bEmptyV : L::bEmptyK, L::bLand, is_v,
-                                           base + (is_v ? L::kRingV : L::kRingK)};
+                                           base + (is_v ? L::kRingV : L::kRingK),
+                                RingPos(L::kSlots)};
             int q = 0;
             for (;; ++q) {
                 Seg s;
@@ -353,7 +387,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     ptx::mbar_arrive_expect_tx(ctl.bar(L::bQFull + b),
                                                (uint32_t)(a.tile_rows * a.group * 128 * L::kPanels));
                     for (int p = 0; p < L::kPanels; ++p)
-                        ptx::tma_load_3d(base + L::kQ0 + b * L::kQ + p * kQPanel, &tmQ, ctl.bar(L::bQFull + b), p * 64,
+                        ptx::tma_load_3d(base + L::kQ0 + b * L::kQ + p * L::kQPanel, &tmQ, ctl.bar(L::bQFull + b), p * 64,
                                          s.head * a.group, s.row0);
                 }
                 if (!feed.tiles(a.table + (long long)s.seq * a.max_pages, a.page_shift, a.n_pages, s.kt0, s.n, s.seen,
@@ -368,11 +402,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     } else if (warp == 2) {
         // ------------------------------------------------------------ MMA issuer
         if (elect_one()) {
-            constexpr uint32_t idesc_qk = ptx::idesc_bf16(BM, BN, false, false);
-            constexpr uint32_t idesc_pv = ptx::idesc_bf16(BM, HD, false, true);
-            RingPos<L::kSlots> kp, vp;
+            constexpr uint32_t idesc_qk = ptx::idesc_bf16(L::kM, BN, false, false);
+            constexpr uint32_t idesc_pv = ptx::idesc_bf16(L::kM, HD, false, true);
+            RingPos kp(L::kSlots), vp(L::kSlots);
             int steps[2] = {0, 0}, uses[2] = {0, 0};   // tiles and segments of each stream so far
-            bool ok = true;
+            bool ok = ctl.poll(L::bZeros, 0);
             for (int q = 0; ok; ++q) {
                 Seg s;
                 if (!take(q, s) || s.n == 0) break;
@@ -417,7 +451,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                             const uint32_t kd = desc_lo(base + L::kRingK + kp.slot * L::kTile, 16);
 #pragma unroll
                             for (int kk = 0; kk < HD / 16; ++kk)
-                                mma_ss(tmem + tmem_s(st), qd - st * (kQPanel >> 4) + (((kk >> 2) * kQPanel + (kk & 3) * 32) >> 4),
+                                mma_ss(tmem + tmem_s(st), qd - st * (L::kQRows >> 4) + (((kk >> 2) * L::kQPanel + (kk & 3) * 32) >> 4),
                                        kd + (((kk >> 2) * kPanel + (kk & 3) * 32) >> 4), idesc_qk, kk > 0);
                             ptx::mma_commit(ctl.bar(L::bSFull + st));
                             ptx::mma_commit(ctl.bar(L::bEmptyK + kp.slot));
@@ -433,6 +467,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         }
     } else if (warp == 3) {
         // ------------------------------------------------------------ V rows past the last key
+        clear_around_q();
         int tiles = 0;
         uint32_t land_phase = 0;                       // by slot: parity of its next phase
         for (int q = 0;; ++q) {
@@ -459,6 +494,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const uint32_t tS = tmem + lane_off + tmem_s(st), tO = tmem + lane_off + tmem_o(st);
         float* stage = reinterpret_cast<float*>(gbase) + lane * L::kStageRow;
         volatile float2* stage_ml = reinterpret_cast<volatile float2*>(gbase + L::kStageMl) + lane;
+        clear_around_q();
         int done_steps = 0, uses = 0;
         for (int q = 0;; ++q) {
             Seg s;
@@ -472,7 +508,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             // steps whose tile every row sees whole; the rest is masked
             const int whole = __reduce_min_sync(0xFFFFFFFFu, limit) - first - BN;
             const int plain = whole < 0 ? 0 : min(steps, whole / (2 * BN) + 1);
-            float m = -INFINITY, l = 0.f;
+            // lanes past the R rows hold no row: no logit passes their maximum
+            float m = R == 32 || lane < R ? -INFINITY : INFINITY, l = 0.f;
             int j = 0;
             for (; j < steps; ++j) {
                 if (!ctl.warp_poll(L::bSFull + st, (done_steps + j) & 1)) break;
@@ -561,17 +598,21 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 }
 
 // Adds the parts of the items that shares cut.  Block b looks at the boundary
-// between CTA b and CTA b + 1 and, if it is the first one inside its item,
-// merges that item's rows, a warp per row: parts in the CTAs' order.
+// between CTA b and CTA b + 1; the blocks whose boundaries lie inside one item
+// take its rows in turn.  One to eight warps per row, by the number of its
+// parts: each adds some of them in the CTAs' order, then one adds the sums.
+// (One block per item, a warp per row, took 50 us of 66 for 32 rows of 32 parts.)
 template <int HD>
 __global__ void __launch_bounds__(256)
 paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
     constexpr int E = HD / 32;
+    __shared__ float2 sum_ml[8];
+    __shared__ float sum_o[8][HD];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the lists are inputs: they may be read before the attention kernel is done
     const Shares sh(all_tiles(a, false), ctas);
     const int c = (int)blockIdx.x + 1;
-    int row0 = 0, rows = 0, head = 0, last_cta = 0;
+    int row0 = 0, rows = 0, head = 0, first = 0, last = 0;     // CTAs whose boundaries cut the item
     if (c < sh.n) {
         const int cut = sh.begin(c);
         int at = 0;
@@ -587,12 +628,11 @@ paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
                 const int tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, j);
                 head = (cut - f) / tiles;
                 const int item = f + head * tiles;
-                // the first cut inside the item, and not its beginning
-                if (cut > item && sh.begin(c - 1) <= item) {
+                if (cut > item) {                              // inside the item, not its beginning
                     row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, j);
-                    rows = __shfl_sync(0xFFFFFFFFu, mine.rows, j);
-                    last_cta = c;
-                    while (last_cta + 1 < sh.n && sh.begin(last_cta + 1) < item + tiles) ++last_cta;
+                    rows = __shfl_sync(0xFFFFFFFFu, mine.rows, j) * a.group;
+                    first = sh.owner(item) + 1;
+                    last = sh.owner(item + tiles - 1);
                 }
                 break;
             }
@@ -601,19 +641,18 @@ paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (rows == 0) return;
-    const int parts = last_cta - c + 2;                // CTA c - 1's last part, then the first of c .. last_cta
-    auto slot_of = [&](int p) { return p == 0 ? 2ll * (c - 1) + 1 : 2ll * (c - 1 + p); };
-    for (int r = warp; r < rows * a.group; r += 8) {
+    const int parts = last - first + 2;                        // CTA first - 1's last part, then the first of the others
+    auto slot_of = [&](int p) { return p == 0 ? 2ll * (first - 1) + 1 : 2ll * (first - 1 + p); };
+    const int width = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;      // warps per row
+    const int per_block = 8 / width;
+    // (every warp of the block makes the same number of rounds)
+    for (int r0 = (c - first) * per_block; r0 < rows; r0 += (last - first + 1) * per_block) {
+        const int r = r0 + warp / width;
         float M = -INFINITY, acc[E], sum = 0.f;
         bool missing = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        // one pass, relative to the largest m so far: the loads of four parts are in flight together
-#pragma unroll 4
-        for (int p = 0; p < parts; ++p) {
-            const long long at = slot_of(p) * a.part_rows + r;
-            const float2 ml = a.part_ml[at];
-            const float* src = a.part_o + at * HD + lane * E;
+        auto add = [&](float2 ml, const float* src) {
             float x[E];
             if constexpr (E == 4) {
                 const float4 v = *reinterpret_cast<const float4*>(src);
@@ -631,8 +670,25 @@ paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
                 for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e] * old);
                 M = top;
             }
+        };
+        if (r < rows) {
+            // one pass, relative to the largest m so far: the loads of four parts are in flight together
+#pragma unroll 4
+            for (int p = warp % width; p < parts; p += width) {
+                const long long at = slot_of(p) * a.part_rows + r;
+                add(a.part_ml[at], a.part_o + at * HD + lane * E);
+            }
         }
-        if (missing) continue;                                 // JANO_ETIMEOUT was raised
+        if (width > 1) {
+            if (lane == 0) sum_ml[warp] = make_float2(M, missing ? -1.f : sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) sum_o[warp][lane * E + e] = acc[e];
+            __syncthreads();
+            if (warp % width == 0)
+                for (int p = 1; p < width; ++p) add(sum_ml[warp + p], &sum_o[warp + p][lane * E]);
+            __syncthreads();
+        }
+        if (warp % width || r >= rows || missing) continue;    // missing: JANO_ETIMEOUT was raised
         const float inv = sum != 0.f ? 1.0f / sum : 0.f;
         __nv_bfloat16* dst = a.out + (long long)(row0 + r / a.group) * a.out_ld +
                              (head * a.group + r % a.group) * HD + lane * E;
@@ -651,23 +707,24 @@ long long max_tiles(const PagedAttentionCall& c) {
     return ((len + BN - 1) / BN + 1) * c.seqs->n_seqs * c.pool->kv_heads;
 }
 
-template <int HD>
-cudaError_t launch_hd(const PagedAttentionCall& c, Args& a, int ctas, cudaStream_t st) {
-    using L = Layout<HD>;
+template <int HD, int R>
+cudaError_t launch_form(const PagedAttentionCall& c, Args& a, int ctas, cudaStream_t st) {
+    using L = Layout<HD, R>;
     static DeviceOnce ready;
     int dev = 0;
     cudaGetDevice(&dev);
     if (!ready.done(dev)) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<HD>,
+        const cudaError_t e = cudaFuncSetAttribute(paged_decode_kernel<HD, R>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kAlloc);
         if (e != cudaSuccess) return e;
         ready.mark(dev);
     }
+    a.tile_rows = R / a.group;
     CUtensorMap mq, mk, mv;
     if (!make_q_map(&mq, c.q, c.q_ld, c.n_rows, c.heads, HD, a.group, a.tile_rows) ||
         !make_pool_map(&mk, c.pool->k, *c.pool) || !make_pool_map(&mv, c.pool->v, *c.pool))
         return cudaErrorInvalidValue;
-    paged_decode_kernel<HD><<<ctas, kThreads, L::kAlloc, st>>>(mq, mk, mv, a);
+    paged_decode_kernel<HD, R><<<ctas, kThreads, L::kAlloc, st>>>(mq, mk, mv, a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || ctas == 1) return e;
     cudaLaunchConfig_t cfg{};
@@ -686,7 +743,7 @@ cudaError_t launch_hd(const PagedAttentionCall& c, Args& a, int ctas, cudaStream
 
 size_t paged_decode_workspace_bytes(int max_rows, int heads, int kv_heads, int d, int sms) {
     const long long rows = (long long)max_rows * (heads / kv_heads);
-    if (rows > kRows) return 0;
+    if (rows > kMaxRows) return 0;
     return (size_t)2 * sms * rows * (d + 2) * sizeof(float);
 }
 
@@ -708,7 +765,6 @@ cudaError_t launch_paged_decode(const PagedAttentionCall& c, int sms, int* err, 
     a.max_len = c.max_len < room ? c.max_len : (int)room;
     a.kv_heads = c.pool->kv_heads;
     a.group = c.heads / c.pool->kv_heads;
-    a.tile_rows = kRows / a.group;
     a.scale_log2 = c.scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(c.out);
     a.out_ld = c.out_ld;
@@ -719,7 +775,9 @@ cudaError_t launch_paged_decode(const PagedAttentionCall& c, int sms, int* err, 
     // no more CTAs than key tiles that the bounds allow
     const long long most = max_tiles(c);
     const int ctas = (int)(most < sms ? most : sms);
-    return c.pool->d == 128 ? launch_hd<128>(c, a, ctas, st) : launch_hd<64>(c, a, ctas, st);
+    if (a.part_rows <= 16)
+        return c.pool->d == 128 ? launch_form<128, 16>(c, a, ctas, st) : launch_form<64, 16>(c, a, ctas, st);
+    return c.pool->d == 128 ? launch_form<128, 32>(c, a, ctas, st) : launch_form<64, 32>(c, a, ctas, st);
 }
 
 }  // namespace jano

@@ -123,22 +123,23 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 
 // The ring of K or of V tiles in shared memory, as its producer or its consumer
 // counts through it.
-template <int kSlots>
 struct RingPos {
+    int slots;
     int slot = 0, phase = 0;
+    __device__ __forceinline__ explicit RingPos(int n) : slots(n) {}
     __device__ __forceinline__ void advance() {
-        if (++slot == kSlots) {
+        if (++slot == slots) {
             slot = 0;
             phase ^= 1;
         }
     }
 };
 
-// One thread's feed of one operand (K or V) into its ring of kSlots tiles, by
+// One thread's feed of one operand (K or V) into its ring of tiles, by
 // page-sized copies.  K and V have a producer each: a lone thread runs some
 // five cycles per instruction, and one producer for both took 1,300 cycles per
 // 32 KB tile (page ids, bounds, barrier, coordinates), as long as the copy.
-template <int HD, int kSlots, bool kSpin>
+template <int HD, bool kSpin>
 struct Feed {
     static constexpr int kPanels = HD / 64;
     const Ctl& ctl;
@@ -146,7 +147,7 @@ struct Feed {
     int b_full, b_empty, b_land;       // barriers; the ragged last V tile lands on b_land (K: b_full) ...
     bool is_v;                         // ... and is cleared past its last key before b_full
     uint32_t ring;
-    RingPos<kSlots> pos;
+    RingPos pos;
     uint32_t landing = 0, land_phase = 0;      // by slot: last load went to b_land; parity of its next phase
     int loads = 0;
 
@@ -210,13 +211,13 @@ struct Feed {
     }
     // Every copy that was issued lands before the CTA's shared memory is released.
     __device__ __forceinline__ void drain() {
-        for (int k = 0; k < kSlots; ++k) {
+        for (int k = 0; k < pos.slots; ++k) {
             const int before = loads - 1 - k;          // loads counted back from the last
             if (before < 0) break;
-            const int at = before % kSlots;
+            const int at = before % pos.slots;
             const bool land = (landing >> at) & 1u;
             if (!ptx::mbar_wait(ctl.bar((land ? b_land : b_full) + at),
-                                land ? ((land_phase >> at) & 1u) ^ 1u : (before / kSlots) & 1, kWaitLimit))
+                                land ? ((land_phase >> at) & 1u) ^ 1u : (before / pos.slots) & 1, kWaitLimit))
                 break;
         }
     }
@@ -253,9 +254,9 @@ __device__ __forceinline__ float exp64(const uint32_t (&s)[64], float c, float n
 // One key tile of one tile row (see the file comments): S from TMEM, maximum,
 // lazy rescale of O, P back as BF16.  With `masked` (the same in the whole
 // warp) the row sees the tile's first `valid` keys only: the other logits
-// become -inf, whatever S holds there, and their P exactly 0.  One body for
-// both kinds of tile: a second copy would cost each CTA the instruction fetch
-// of 20 KB at its last tile.
+// become -inf, whatever S holds there, and their P exactly 0.  The decode form
+// passes it at run time: there a second copy would cost each CTA the
+// instruction fetch of 20 KB at its last tile.
 template <int HD>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, bool masked, int valid, float c, float& m, float& l,
                                              uint32_t bar_half) {
@@ -277,8 +278,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, bool masked, int valid
     const bool want = mxs > m + 8.0f;
     if (__any_sync(0xFFFFFFFFu, want)) {
         const float m_new = want ? mxs : m;
-        // nothing to rescale while no row of the warp has seen a key
-        if (__any_sync(0xFFFFFFFFu, m > -INFINITY)) {
+        // nothing to rescale while no row of the warp has seen a key (m = -inf;
+        // a lane without a row has m = inf)
+        if (__any_sync(0xFFFFFFFFu, fabsf(m) < INFINITY)) {
             const float alpha = want ? ptx::ex2(m - m_new) : 1.0f;
             l *= alpha;
 #pragma unroll 1
@@ -329,12 +331,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
+            const cuuint32_t* box, CUtensorMapL2promotion fetch) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint32_t es[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, fetch,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -343,7 +345,7 @@ bool make_q_map(CUtensorMap* m, const void* q, long long ld, int n_rows, int hea
     const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n_rows};
     const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_rows};
-    return encode(m, q, 3, dims, strides, box);
+    return encode(m, q, 3, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 // The pool [page][place][head][d] with its own strides: a box is up to 128 places of one page and head x 64 columns.
@@ -353,7 +355,10 @@ bool make_pool_map(CUtensorMap* m, const void* pages, const jano_page_pool& p) {
     const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, (cuuint64_t)p.head_stride * 2,
                                    (cuuint64_t)p.page_stride * 2};
     const cuuint32_t box[4] = {64, (cuuint32_t)(p.page_size < BN ? p.page_size : BN), 1, 1};
-    return encode(m, pages, 4, dims, strides, box);
+    // L2 fetches a head's row at once, and not its neighbour's: with 256 bytes
+    // for d = 64, 32 sequences of 8,192 tokens (token-major) took 139 us, not 100
+    return encode(m, pages, 4, dims, strides, box,
+                  p.d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 }  // namespace
