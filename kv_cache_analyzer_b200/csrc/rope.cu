@@ -8,15 +8,21 @@
 //   (x0, x1) -> (x0 c - x1 s, x0 s + x1 c),
 // in fp32 with one rounding to BF16; columns past rot are moved bit for bit.
 //
-// Pure HBM streaming: every row is read once and written once.  One warp
-// takes one row (or, when there are too few rows to fill the SMs, a part of
-// one) of one of up to three tensors (q, k, v: one launch for all), resolves
-// the row's place and coordinates once, and walks its heads 32 units at a
-// time.  A unit is the 16-byte vector of 4 adjacent pairs (interleaved
-// pairing) or the two vectors that hold 8 split pairs (halves pairing), so a
-// pair never crosses lanes.  Where the units of a head divide 32 (d = 64 and
-// 128 rotated whole, among others) a lane meets the same slots in every head
-// and keeps its cos and sin in registers for the whole row.
+// Every row is read once and written once: bound by HBM, and close behind by
+// the issue of instructions, so addresses go up by constants and the pairs are
+// turned two at a time.  One warp takes one row (or, when there are too few
+// rows to fill the SMs, a part of one) of one of up to three tensors (q, k, v:
+// one launch for all), resolves the row's place and coordinates once, and
+// walks its heads 32 units at a time.  A unit is the 16-byte vector of 4
+// adjacent pairs (interleaved pairing) or the two vectors that hold 8 split
+// pairs (halves pairing), so a pair never crosses lanes.  Where the units of a
+// head divide 32 (d = 64 and 128 rotated whole, among others) a lane meets the
+// same slots in every head and keeps its cos and sin in registers for the
+// whole row.
+//
+// 18,900 rows of 40 heads of 128 (387 MB): 61.6 us, 6.3 TB/s; Q, K and V of
+// 11,466 rows of 12 heads of 128 into the cache (211 MB): 35.1 us, 6.0 TB/s,
+// into pages 37.7 us; a few rows: 2.5 us, the launch.
 #include <cuda_bf16.h>
 
 #include "jano_common.cuh"
@@ -161,19 +167,28 @@ __device__ __forceinline__ void load_cs(const Tab& t, const int (&p)[3], int slo
     }
 }
 
-// The 4 adjacent pairs of a vector; pairs from slot `live` on are kept.
+// The 4 adjacent pairs of a vector, two at a time in packed fp32; pairs from
+// slot `live` on are kept.  (The issue of instructions counts next to the
+// bytes here: 35.1 us for the Q, K and V of 11,466 rows, 36.9 pair by pair.)
 __device__ __forceinline__ uint4 turn_pairs(uint4 x, const float (&c)[4], const float (&s)[4], int live) {
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float x0 = lo_f(w[i]), x1 = hi_f(w[i]);
-        const uint32_t y = ptx::pack_bf16(fmaf(x0, c[i], -(x1 * s[i])), fmaf(x0, s[i], x1 * c[i]));
-        if (i < live) w[i] = y;
+    for (int i = 0; i < 4; i += 2) {
+        const uint64_t x0 = ptx::f2(lo_f(w[i]), lo_f(w[i + 1])), x1 = ptx::f2(hi_f(w[i]), hi_f(w[i + 1]));
+        const uint64_t cc = ptx::f2(c[i], c[i + 1]), ss = ptx::f2(s[i], s[i + 1]);
+        float a0, b0, a1, b1;
+        ptx::f2split(ptx::ffma2(x0, cc, ptx::fmul2(x1, ptx::f2(-s[i], -s[i + 1]))), a0, b0);
+        ptx::f2split(ptx::ffma2(x0, ss, ptx::fmul2(x1, cc)), a1, b1);
+        const uint32_t ya = ptx::pack_bf16(a0, a1), yb = ptx::pack_bf16(b0, b1);
+        if (i < live) w[i] = ya;
+        if (i + 1 < live) w[i + 1] = yb;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The 8 split pairs of two vectors (first and second half of the rotated columns).
+// The 8 split pairs of two vectors (first and second half of the rotated
+// columns), one by one: packed, the registers cost more than the issue gains
+// (18,900 rows of 12 heads of 128: 23.9 us, packed 24.9).
 __device__ __forceinline__ void turn_halves(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8]) {
     uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -192,9 +207,9 @@ __device__ __forceinline__ void turn_halves(uint4& a, uint4& b, const float (&c)
 template <bool kHalves, bool kFixed>
 __global__ void __launch_bounds__(kWarps * 32)
 rope_rows_kernel(const __grid_constant__ Args a) {
-    // units in flight per lane: 8 vectors, the whole of a row of 12 heads of 128
-    // (18,900 rows of 40 heads: 67.2 us with 4, 66.9 with 8)
-    constexpr int kUnroll = kHalves ? 4 : 8;
+    // units in flight per lane: more cost occupancy, fewer leave gaps (Q, K and V
+    // of 11,466 rows of 12 heads of 128: 36.5 us with 4, 35.1 with 6, 41.0 with 8)
+    constexpr int kUnroll = kHalves ? 4 : 6;
     const int lane = threadIdx.x & 31;
     const unsigned item = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const unsigned rj = item / (unsigned)a.parts;
@@ -217,20 +232,24 @@ rope_rows_kernel(const __grid_constant__ Args a) {
     if (begin >= end) return;
 
     const uint4* src = jb.src + (long long)r * jb.src_ld;
-    // source offset of unit e (heads are adjacent in a source row); the second
-    // vector of a split pair lies half_vec further on
-    auto unit_of = [&](int e) { return kFixed ? (lane & (units - 1)) : e % units; };
-    auto src_of = [&](int e, int u) {
-        return (e - u) / units * a.d_vec + (split && u >= half_vec ? u + half_vec : u);
-    };
+    // Unit e is unit e % units of head e / units; the second vector of a split
+    // pair lies half_vec further on.  kFixed: 32 units on, the same unit of a
+    // later head, so both addresses go up by constants (the division by a
+    // runtime `units` for every unit kept 71% of the issue slots busy).
+    const int shift = kFixed ? __ffs(units) - 1 : 0;
+    auto head_of = [&](int e) { return kFixed ? e >> shift : e / units; };
+    auto col_of = [&](int u) { return split && u >= half_vec ? u + half_vec : u; };
+    const int my_unit = kFixed ? lane & (units - 1) : 0, my_col = col_of(my_unit);
+    const int src_step = kFixed ? (32 >> shift) * a.d_vec : 0;
     uint4 x[kUnroll], y[kHalves ? kUnroll : 1];
     auto load = [&](int e0) {
+        const uint4* at = kFixed ? src + head_of(e0) * a.d_vec + my_col : src;
 #pragma unroll
         for (int q = 0; q < kUnroll; ++q) {
             const int e = e0 + 32 * q;
             if (e < end) {
-                const int u = unit_of(e);
-                const uint4* s = src + src_of(e, u);
+                const int u = kFixed ? my_unit : e % units;
+                const uint4* s = kFixed ? at + q * src_step : src + head_of(e) * a.d_vec + col_of(u);
                 x[q] = *s;
                 if (kHalves && split && u < half_vec) y[q] = s[half_vec];
             }
@@ -244,16 +263,17 @@ rope_rows_kernel(const __grid_constant__ Args a) {
     if (!resolve(a, r, id, id_before, rot, p, base)) return;
     uint4* dst = jb.dst + (jb.cached ? base : (long long)r * jb.dst_ld);
     float c[kN], s[kN];
-    if (kFixed && rot) load_cs<kN>(a.tab, p, (lane & (units - 1)) * kN, c, s);
+    if (kFixed && rot) load_cs<kN>(a.tab, p, my_unit * kN, c, s);
 
+    const long long dst_step = kFixed ? (32 >> shift) * jb.dst_head : 0;
     for (;;) {
+        uint4* at = kFixed ? dst + head_of(e0) * jb.dst_head + my_col : dst;
 #pragma unroll
         for (int q = 0; q < kUnroll; ++q) {
             const int e = e0 + 32 * q;
             if (e >= end) continue;
-            const int u = unit_of(e);
-            const int v = split && u >= half_vec ? u + half_vec : u;
-            uint4* d = dst + (long long)((e - u) / units) * jb.dst_head + v;
+            const int u = kFixed ? my_unit : e % units;
+            uint4* d = kFixed ? at + q * dst_step : dst + head_of(e) * jb.dst_head + col_of(u);
             if (rot) {
                 if (!kFixed) load_cs<kN>(a.tab, p, u * kN, c, s);
                 if constexpr (kHalves) {
