@@ -21,6 +21,7 @@ import torch
 from . import (Geometry, _stream, _torch_stream, jano_axis_rope, jano_paged_append, jano_paged_attention,
                jano_paged_attention_workspace_bytes, jano_rope_cfg, jano_rope_scatter, jano_rope_table)
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 # the C structures, packed in one step (a fifth of the time of their constructors)
 _ROPE = struct.Struct("9i").pack            # jano_rope_cfg
@@ -34,7 +35,7 @@ def _device(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     if dev != cur:
         raise ValueError(f"{name} is on cuda:{dev}, the current device is cuda:{cur}")
     return dev
@@ -74,12 +75,17 @@ def _shape3(t: torch.Tensor, name: str) -> tuple:
 
 
 def _new(stream, shape, like: torch.Tensor) -> torch.Tensor:
-    """A new BF16 tensor for a launch on `stream` (allocated there, so that the
-    memory's earlier uses are ordered before it)."""
+    """A new tensor of like's type for a launch on `stream` (allocated there, so
+    that the memory's earlier uses are ordered before it)."""
     if stream is None:
-        return like.new_empty(shape)
+        return torch.empty_like(like) if like.shape == shape and like.is_contiguous() else like.new_empty(shape)
     with torch.cuda.stream(_torch_stream(stream)):
         return like.new_empty(shape)
+
+
+def _launch_stream(stream, dev: int) -> int:
+    """The cudaStream_t of a launch on the current device `dev`."""
+    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 def _pool(k_pages: torch.Tensor, v_pages: torch.Tensor, dev: int) -> bytes:
@@ -171,7 +177,7 @@ def axis_rope(x, rope: Rope, table, ids=None, coords=None, out=None, stream=None
         out = _new(stream, (n, h, d), x)
     o_ptr, o_ld = _rows(out, "out", dev, n, h, d)
     jano_axis_rope(x_ptr, x_ld, _list(ids, "ids", n, dev), _list(coords, "coords", 3 * n, dev), n, h, d,
-                   rope.packed(), _list(table, "table", 2 * rope.entries, dev, _F32), o_ptr, o_ld, _stream(stream))
+                   rope.packed(), _list(table, "table", 2 * rope.entries, dev, _F32), o_ptr, o_ld, _launch_stream(stream, dev))
     return out
 
 
@@ -205,7 +211,7 @@ def rope_scatter(k, v, idx, k_cache, v_cache, rope: Rope, table, q=None, q_out=N
                       _list(coords, "coords", 3 * n, dev), n, heads, h, d, rope.packed(),
                       _list(table, "table", 2 * rope.entries, dev, _F32), o_ptr, o_ld,
                       _list(k_cache, "k_cache", size, dev, _BF16), _list(v_cache, "v_cache", size, dev, _BF16), N,
-                      _stream(stream))
+                      _launch_stream(stream, dev))
     return q_out
 
 
@@ -245,7 +251,7 @@ def paged_append(k, v, pos, k_pages, v_pages, page_table, seq_lens, cu_rows, rop
     jano_paged_append(_pool(k_pages, v_pages, dev), seqs, q_ptr, q_ld, k_ptr, k_ld, v_ptr, v_ld,
                       _list(pos, "pos", n, dev), _list(coords, "coords", 3 * n, dev),
                       _list(grids, "grids", 2 * page_table.shape[0], dev), n, heads, cfg, table, o_ptr, o_ld,
-                      _stream(stream))
+                      _launch_stream(stream, dev))
     return q_out
 
 
@@ -291,5 +297,5 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_rows, out=None
             ws = workspace.data_ptr()
     jano_paged_attention(pool, _seqs(page_table, seq_lens, cu_rows, dev), q_ptr, q_ld,
                          _list(limits, "limits", n, dev), n, max_rows, max_len, h,
-                         d ** -0.5 if scale is None else scale, split, ws, ws_bytes, o_ptr, o_ld, _stream(stream))
+                         d ** -0.5 if scale is None else scale, split, ws, ws_bytes, o_ptr, o_ld, _launch_stream(stream, dev))
     return out
