@@ -157,14 +157,6 @@ __device__ __forceinline__ int warp_sum_to(int v) {    // inclusive prefix sum o
     }
     return v;
 }
-// Key tiles of all sequences and heads (the whole warp); the launcher has
-// checked that they fit an int.
-__device__ __forceinline__ int all_tiles(const Args& a, bool report) {
-    int total = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 32)
-        total += __reduce_add_sync(0xFFFFFFFFu, seq_info(a, s0 + (threadIdx.x & 31), report).tiles);
-    return total * a.kv_heads;
-}
 // Equal shares of the tiles, the first `more` ones a tile longer; no more
 // shares than give each of them two tiles.
 struct Shares {
@@ -174,6 +166,43 @@ struct Shares {
     __device__ int owner(int tile) const {         // the share that a tile lies in
         const int long_ones = more * (each + 1);
         return tile < long_ones ? tile / (each + 1) : more + (tile - long_ones) / each;
+    }
+};
+
+// Shares that end with their (sequence, head): each is one of the parts of
+// some `quota` tiles that its item is cut into.  Taken where it costs at most
+// two tiles more than equal shares of everything: a CTA that goes on to a second
+// item drains and fills its pipeline in between, as long as three tiles take
+// (one token of 24 heads over 4,096 tokens: the CTAs that cross ended after 15
+// to 17 us, the others after 12 to 14; 21.3 us in all, 19.3 without crossing).
+// Parts of an item of `tiles` (a float quotient: what this computes counts).
+__device__ __forceinline__ int item_parts(int tiles, int quota) {
+    return min(tiles, max(1, (int)ceilf(__fdividef((float)tiles, (float)quota) - 0.001f)));
+}
+// The quota, 0 for equal shares.  The whole warp; n_seqs <= 32, `tiles` the lane's sequence's.
+__device__ __forceinline__ int item_quota(const Args& a, int tiles, const Shares& sh, int ctas) {
+    const int least = max(2, sh.each + (sh.more > 0));
+    int quota = 0;
+#pragma unroll 1
+    for (int t = least + 2; t >= least && a.n_seqs <= 32; --t) {   // most often the first is one too many
+        if (__reduce_add_sync(0xFFFFFFFFu, item_parts(tiles, t)) * a.kv_heads > ctas) break;
+        quota = t;
+    }
+    return quota;
+}
+// Share c of those: its sequence (a lane), head, part of how many; the item's first share.
+struct ItemPart {
+    int lane, head, part, parts, first;
+    __device__ __forceinline__ ItemPart(const Args& a, int tiles, int quota, int c) {
+        const int mine = item_parts(tiles, quota);
+        const int upto = warp_sum_to(mine), from = (upto - mine) * a.kv_heads;
+        lane = __ffs(__ballot_sync(0xFFFFFFFFu, c >= from && c < from + mine * a.kv_heads)) - 1;
+        if (lane < 0) return;                              // no such share
+        parts = __shfl_sync(0xFFFFFFFFu, mine, lane);
+        const int rem = c - __shfl_sync(0xFFFFFFFFu, from, lane);
+        head = rem / parts;
+        part = rem - head * parts;
+        first = c - part;
     }
 };
 
@@ -187,15 +216,34 @@ struct Walk {
     unsigned todo;                         // lanes whose sequences are still to come
     Seg s;
     int tiles, first, item;                // of the sequence in hand; the item's first tile (< end: there is one)
+    bool one;                              // the share is s alone (item_quota), not yet handed out
 
-    // `all`: key tiles of every sequence and head, from the walk's own first look
-    __device__ __forceinline__ Walk(const Args& args, bool report) : a(args), s0(0), at(0), todo(0), tiles(0), first(0), item(0) {
+    __device__ __forceinline__ Walk(const Args& args, bool report) : a(args), s0(0), at(0), upto(0), todo(0), tiles(0), first(0), item(0), one(false) {
         const int lane = threadIdx.x & 31;
         mine = seq_info(a, lane, report);
         int total = __reduce_add_sync(0xFFFFFFFFu, mine.tiles);
         for (int k = 32; k < a.n_seqs; k += 32)
             total += __reduce_add_sync(0xFFFFFFFFu, seq_info(a, k + lane, report).tiles);
         const Shares sh(total * a.kv_heads, (int)gridDim.x);
+        if (const int quota = item_quota(a, mine.tiles, sh, (int)gridDim.x)) {
+            begin = end = 0;
+            s.head = a.kv_heads;
+            const ItemPart it(a, mine.tiles, quota, (int)blockIdx.x);
+            if (it.lane < 0) return;
+            one = true;
+            tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, it.lane);
+            s.row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, it.lane);
+            s.rows = __shfl_sync(0xFFFFFFFFu, mine.rows, it.lane);
+            s.seen = __shfl_sync(0xFFFFFFFFu, mine.seen, it.lane);
+            s.seq = it.lane;
+            s.head = it.head;
+            const int each = tiles / it.parts, more = tiles - each * it.parts;
+            s.kt0 = it.part * each + min(it.part, more);
+            s.n = each + (it.part < more);
+            s.part = it.parts > 1 ? 0 : -1;
+            s0 = 32;
+            return;
+        }
         begin = end = 0;
         if ((int)blockIdx.x < sh.n) {
             begin = sh.begin(blockIdx.x);
@@ -210,6 +258,10 @@ struct Walk {
         todo = __ballot_sync(0xFFFFFFFFu, mine.tiles > 0 && from < end && from + mine.tiles * a.kv_heads > begin);
     }
     __device__ __forceinline__ bool next() {
+        if (one) {
+            one = false;
+            return true;
+        }
         if (s.head + 1 < a.kv_heads && item + tiles < end) {       // the next head of the sequence in hand
             ++s.head;
             item += tiles;
@@ -610,14 +662,29 @@ paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
     __shared__ float sum_o[8][HD];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the lists are inputs: they may be read before the attention kernel is done
-    const Shares sh(all_tiles(a, false), ctas);
+    SeqInfo mine = seq_info(a, lane, false);
+    int total = __reduce_add_sync(0xFFFFFFFFu, mine.tiles);
+    for (int k = 32; k < a.n_seqs; k += 32)
+        total += __reduce_add_sync(0xFFFFFFFFu, seq_info(a, k + lane, false).tiles);
     const int c = (int)blockIdx.x + 1;
-    int row0 = 0, rows = 0, head = 0, first = 0, last = 0;     // CTAs whose boundaries cut the item
-    if (c < sh.n) {
+    // the item's rows and head, its parts, and where they lie: slot0, then 2 (base + p)
+    int row0 = 0, rows = 0, head = 0, parts = 0, slot0 = 0, base = 0, turn = 0;
+    const Shares sh(total * a.kv_heads, ctas);
+    if (const int quota = item_quota(a, mine.tiles, sh, ctas)) {
+        const ItemPart it(a, mine.tiles, quota, c);
+        if (it.lane >= 0 && it.part > 0) {
+            row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, it.lane);
+            rows = __shfl_sync(0xFFFFFFFFu, mine.rows, it.lane) * a.group;
+            head = it.head;
+            parts = it.parts;
+            turn = it.part - 1;
+            base = it.first;
+            slot0 = 2 * base;
+        }
+    } else if (c < sh.n) {
         const int cut = sh.begin(c);
-        int at = 0;
-        for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-            const SeqInfo mine = seq_info(a, s0 + lane, false);
+        for (int s0 = 0, at = 0; s0 < a.n_seqs; s0 += 32) {
+            if (s0) mine = seq_info(a, s0 + lane, false);
             const int upto = warp_sum_to(mine.tiles);
             const int next = at + __shfl_sync(0xFFFFFFFFu, upto, 31) * a.kv_heads;
             if (cut < next) {
@@ -631,8 +698,10 @@ paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
                 if (cut > item) {                              // inside the item, not its beginning
                     row0 = __shfl_sync(0xFFFFFFFFu, mine.row0, j);
                     rows = __shfl_sync(0xFFFFFFFFu, mine.rows, j) * a.group;
-                    first = sh.owner(item) + 1;
-                    last = sh.owner(item + tiles - 1);
+                    base = sh.owner(item);                     // its last part, then the first of the others
+                    slot0 = 2 * base + 1;
+                    parts = sh.owner(item + tiles - 1) - base + 1;
+                    turn = c - base - 1;
                 }
                 break;
             }
@@ -641,12 +710,11 @@ paged_decode_merge_kernel(const __grid_constant__ Args a, int ctas) {
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (rows == 0) return;
-    const int parts = last - first + 2;                        // CTA first - 1's last part, then the first of the others
-    auto slot_of = [&](int p) { return p == 0 ? 2ll * (first - 1) + 1 : 2ll * (first - 1 + p); };
+    auto slot_of = [&](int p) { return p == 0 ? (long long)slot0 : 2ll * (base + p); };
     const int width = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;      // warps per row
     const int per_block = 8 / width;
     // (every warp of the block makes the same number of rounds)
-    for (int r0 = (c - first) * per_block; r0 < rows; r0 += (last - first + 1) * per_block) {
+    for (int r0 = turn * per_block; r0 < rows; r0 += (parts - 1) * per_block) {
         const int r = r0 + warp / width;
         float M = -INFINITY, acc[E], sum = 0.f;
         bool missing = false;

@@ -205,6 +205,10 @@ FEW = [  # at most 32 packed rows per sequence: the form in which every SM takes
     ([8, 8], [600, 90], 12, 3, 64, 16, "random", dict(head_major=True)),
     ([1] * 70, [(s * 97) % 400 + 1 for s in range(70)], 4, 2, 64, 16, None, dict(pad_rows=3)),   # three looks of 32
     ([1] * 40, [1] * 40, 2, 2, 128, 16, None, {}),                     # fewer tiles than SMs
+    ([1] * 20, [(s * 331) % 2200 + 1 for s in range(20)], 16, 8, 64, 16, None, {}),   # 160 items: shares go across them
+    ([1, 2, 1, 1, 3], [4000, 1, 700, 2300, 129], 6, 3, 128, 64, "random", {}),        # shares that end with their item
+    ([1] * 9, [1300] * 8 + [3], 32, 2, 64, 32, None, {}),              # 16 rows: MMAs of 64 rows
+    ([17], [3000], 1, 1, 64, 64, "random", {}),                        # 17: of 128
     ([2, 1, 1], [0, 0, 5], 2, 2, 64, 16, None, dict(one_buffer=True, pad_rows=2)),
     ([3, 3], [300, 200], 6, 2, 128, 32, "dark", {}),                   # a sequence whose rows all see nothing
 ]
