@@ -17,24 +17,31 @@
 //           rows than one tile holds): each K/V tile is read once for both;
 //   single  one query tile, the even key tiles in stream 0 and the odd ones
 //           in stream 1, each with its own running maximum, sum and O, merged
-//           at the end.  This is the form of single tokens, bound by the
-//           cache's bytes: up to four K/V tiles (128 KB for d = 128) are in
-//           flight per SM, and half-empty MMA tiles cost nothing that counts.
+//           at the end: sequences of few rows, where the cache's bytes count
+//           (64 rows each over 8 x 8,192 positions of 24 heads: 148 us, 5.4 TB/s).
 // Which one a CTA takes is decided by its own sequence's rows, so one launch
 // serves single tokens and long chunks together.
 //
 // Few rows leave SMs idle: the key tiles are then cut over the 2 to 8 CTAs
 // of a thread-block cluster, which merge their (O, m, l) through distributed
 // shared memory -- no workspace, no second launch, and a fixed order of sums.
+// (At most 32 packed rows per sequence: paged_decode.cu, where a call brings
+// a workspace.)
+//
+// Bound by the tensor core and the softmax together, and in long runs by the
+// card's power: 16,380 rows over 32,760 positions of 12 heads of 128, pages of
+// 128 places, 3,080 us, 1,070 TFLOP/s, as the contiguous kernel.  Smaller pages
+// are more copies: 4,096 rows over 16,384 positions of 24 heads take 753 us
+// with pages of 256 places, 777 with 64, 818 with 16.
 //
 // 12 warps: 0-3 and 4-7 softmax warpgroups (thread = tile row = TMEM lane),
 // 8 producer of Q and K, 9 MMA issuer, 10 clears V rows past the visible
 // length (stale pages may hold NaN there, and 0 * NaN would reach O), 11
-// producer of V.  A
-// 128-key tile is gathered page by page: one box of min(page_size, 128) rows
-// x 64 columns per page and panel.  The producers and the MMA issuer each run as
-// one elected thread: elect.sync lets the compiler keep their operands in
-// uniform registers, which halved the MMA thread's time per key tile.
+// producer of V.  A 128-key tile is gathered page by page: one box of
+// min(page_size, 128) rows x 64 columns per page and panel.  The producers and
+// the MMA issuer each run as one elected thread: elect.sync lets the compiler
+// keep their operands in uniform registers, which halved the MMA thread's time
+// per key tile.
 // The pool's map has page, head and token strides of its own, so token-major
 // and head-major pools, and K and V inside one allocation, read alike.
 // TMEM columns: S0 [0,128) S1 [128,256) O0 [256,256+d) O1 [384,384+d); P_i is
@@ -482,11 +489,12 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         float m = -INFINITY, l = 0.f;
         int j = 0;
         if (warp_live) {
+            constexpr int kPolyEighths = HD == 64 ? 3 : 0;
             // (two loops: the one body with a branch in it cost 4% of a long chunk's time)
             for (; j < plain; ++j) {
                 if (!ctl.warp_wait(L::bSFull + i, j & 1)) break;
                 ptx::tc_fence_after();
-                softmax_tile<HD>(tS, false, BN, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
+                softmax_tile<HD, kPolyEighths>(tS, false, BN, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + i));
@@ -494,7 +502,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
             for (; j < steps; ++j) {
                 if (!ctl.warp_wait(L::bSFull + i, j & 1)) break;
                 ptx::tc_fence_after();
-                softmax_tile<HD>(tS, true, limit - first - j * apart, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
+                softmax_tile<HD, 0>(tS, true, limit - first - j * apart, a.scale_log2, m, l, ctl.bar(L::bPHalf + i));
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ctl.bar(L::bPFull + i));
@@ -687,9 +695,11 @@ cudaError_t launch_paged_attention(const PagedAttentionCall& c, int* err, cudaSt
     a.err = err;
     const long long tiles = tile_bound(c.n_rows, c.max_rows, c.seqs->n_seqs, a.tile_rows);
     if (tiles > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    // one sequence: its tiles side by side, so that the CTAs at work share the
-    // K/V of few heads in L2.  Several: all heads of the longest tiles first
-    // (four ragged images: measured below)
+    // One sequence: its tiles side by side, so that the CTAs at work share the
+    // K/V of few heads in L2 (4,680 rows over 32,760 positions: 915 us, heads
+    // first 1,048).  Several: all heads of the longest tiles first, so that the
+    // last CTAs are short ones (eight sequences of 500 to 8,000 positions: 440
+    // us, tiles first 485; four images: 144 and 151).
     a.heads_first = c.seqs->n_seqs > 1 && tiles <= 65535;
     return c.pool->d == 128 ? launch_hd<128>(c, a, (int)tiles, err, st) : launch_hd<64>(c, a, (int)tiles, err, st);
 }

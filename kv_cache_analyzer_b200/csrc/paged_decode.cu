@@ -566,7 +566,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             for (; j < steps; ++j) {
                 if (!ctl.warp_poll(L::bSFull + st, (done_steps + j) & 1)) break;
                 ptx::tc_fence_after();
-                softmax_tile<HD>(tS, j >= plain, limit - first - j * 2 * BN, a.scale_log2, m, l,
+                softmax_tile<HD, 0>(tS, j >= plain, limit - first - j * 2 * BN, a.scale_log2, m, l,
                                  ctl.bar(L::bPHalf + st));
                 ptx::tc_fence_before();
                 __syncwarp();

@@ -234,15 +234,48 @@ __device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
     return fmaxf(ptx::fmax3(m[0], m[1], m[2]), ptx::fmax3(m[3], m[4], fmaxf(m[5], fmaxf(m[6], m[7]))));
 }
 
+// 2^x for two lanes on the FMA and ALU pipes, for x <= 8: the range reduction
+// and the cubic of attention.cu (largest relative error 7.5e-5, below the 2^-8
+// rounding of the BF16 P it feeds).
+__device__ __forceinline__ void exp2_poly2(uint64_t x2, float& ya, float& yb) {
+    constexpr float kC0 = 0x1.fff692p-1f, kC1 = 0x1.62f31ap-1f;
+    constexpr float kC2 = 0x1.f0de1ap-3f, kC3 = 0x1.c3f76p-5f;
+    constexpr float kRound = 12582912.0f;            // 1.5 * 2^23
+    float xa, xb;
+    ptx::f2split(x2, xa, xb);
+    x2 = ptx::f2(fmaxf(xa, -125.0f), fmaxf(xb, -125.0f));
+    const uint64_t r2 = ptx::fadd2(x2, ptx::f2(kRound, kRound));     // low bits hold rint(x)
+    const uint64_t t2 = ptx::fadd2(r2, ptx::f2(-kRound, -kRound));
+    const uint64_t f2 = ptx::ffma2(t2, ptx::f2(-1.f, -1.f), x2);      // f = x - rint(x)
+    uint64_t p2 = ptx::ffma2(ptx::f2(kC3, kC3), f2, ptx::f2(kC2, kC2));
+    p2 = ptx::ffma2(p2, f2, ptx::f2(kC1, kC1));
+    p2 = ptx::ffma2(p2, f2, ptx::f2(kC0, kC0));
+    float ra, rb, pa, pb;
+    ptx::f2split(r2, ra, rb);
+    ptx::f2split(p2, pa, pb);
+    const int ja = __float_as_int(ra) - __float_as_int(kRound);
+    const int jb = __float_as_int(rb) - __float_as_int(kRound);
+    ya = __int_as_float(__float_as_int(pa) + (ja << 23));
+    yb = __int_as_float(__float_as_int(pb) + (jb << 23));
+}
+
 // p = 2^(s*c + nm) for 64 values, packed to 32 BF16x2 words; returns sum(p).
+// kPoly of 8 pairs go through exp2_poly2.
+template <int kPoly>
 __device__ __forceinline__ float exp64(const uint32_t (&s)[64], float c, float nm, uint32_t* pk) {
     const uint64_t c2 = ptx::f2(c, c), nm2 = ptx::f2(nm, nm);
     uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
     for (int e = 0; e < 64; e += 2) {
-        float xa, xb;
-        ptx::f2split(ptx::ffma2(ptx::f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nm2), xa, xb);
-        const float a = ptx::ex2(xa), b = ptx::ex2(xb);
+        const uint64_t x2 = ptx::ffma2(ptx::f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), c2, nm2);
+        float a, b;
+        if (((e >> 1) & 7) < kPoly) {
+            exp2_poly2(x2, a, b);
+        } else {
+            ptx::f2split(x2, a, b);
+            a = ptx::ex2(a);
+            b = ptx::ex2(b);
+        }
         acc[(e >> 1) & 3] = ptx::fadd2(acc[(e >> 1) & 3], ptx::f2(a, b));
         pk[e >> 1] = ptx::pack_bf16(a, b);
     }
@@ -257,7 +290,15 @@ __device__ __forceinline__ float exp64(const uint32_t (&s)[64], float c, float n
 // become -inf, whatever S holds there, and their P exactly 0.  The decode form
 // passes it at run time: there a second copy would cost each CTA the
 // instruction fetch of 20 KB at its last tile.
-template <int HD>
+//
+// kPoly: share of the exponentials, in eighths, kept off the MUFU unit.  A tile
+// of 2 x 128 rows keeps it busy for 2,048 cycles and the tensor core for 1,024
+// with d = 64, twice that with d = 128: 4,096 rows over 16,384 keys of 24 heads
+// of 64 take 689, 676, 635, 609, 645 us with 0 to 4 eighths, of 128 alike from
+// 0 to 3 (750 to 800, the power limit).  One warp per stream, as in the decode
+// form, gains nothing (96.2 us of a batch with 0, 96.6 with 2, 103.9 with 3).
+// A masked tile's P must be exactly 0, which the polynomial never is.
+template <int HD, int kPoly>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, bool masked, int valid, float c, float& m, float& l,
                                              uint32_t bar_half) {
     const uint32_t tO = tS + (tmem_o(0) - tmem_s(0)), tP = tS + kTmemP;
@@ -306,13 +347,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, bool masked, int valid
     const float nm = m > -INFINITY ? -m : 0.0f;
     // upper key half first: its P V runs while the lower half is exponentiated
     uint32_t pk[32];
-    l += exp64(hi, c, nm, pk);
+    l += exp64<kPoly>(hi, c, nm, pk);
     ptx::tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(pk));
     ptx::tmem_wait_st();
     ptx::tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar_half);
-    l += exp64(lo, c, nm, pk);
+    l += exp64<kPoly>(lo, c, nm, pk);
     ptx::tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(pk));
     ptx::tmem_wait_st();
 }

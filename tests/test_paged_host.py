@@ -2,6 +2,7 @@
 launch; and the fp64 oracle they are tested against is pinned by hand-worked
 values.  No GPU is needed."""
 import ctypes as C
+import os
 
 import numpy as np
 import pytest
@@ -11,6 +12,7 @@ import kv_cache_analyzer_b200.paged as P
 import oracle.paged as op
 from paged_tools import Paged
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 EINVAL, ESHAPE, EALIGN, EUNSUPPORTED = 1, 2, 3, 4
 
 
@@ -258,6 +260,15 @@ def test_pages_are_handed_out_returned_and_never_shared():
     d = b.open(80)
     t = b.plan([(c, 1), (d, 1)]).lists["page_table"]
     assert t.shape == (2, 5) and len(set(t.flatten().tolist())) == 10
+
+
+# ------------------------------------------------------------------ the polynomial 2^x
+def test_paged_kernels_use_the_tested_polynomial():
+    # tests/test_exp2_poly.py bounds the error of attention.cu's; the paged kernels' is the same text
+    src = os.path.join(ROOT, "kv_cache_analyzer_b200", "csrc")
+    body = [open(os.path.join(src, f)).read().split("void exp2_poly2(")[1].split("\n}\n")[0]
+            for f in ("attention.cu", "paged_tile.cuh")]
+    assert body[0] == body[1]
 
 
 # ------------------------------------------------------------------ oracle pins
