@@ -417,7 +417,7 @@ jano_status jano_paged_attention(const jano_page_pool* pool, const jano_page_seq
     if (s != JANO_OK) return s;
     if (pool->d != 64 && pool->d != 128) return JANO_EUNSUPPORTED;
     if (heads % pool->kv_heads) return JANO_ESHAPE;
-    if (heads / pool->kv_heads > 128 || pool->kv_heads > 65535) return JANO_EUNSUPPORTED;
+    if (heads / pool->kv_heads > 128 || pool->kv_heads > 65535 || max_len > (1 << 26)) return JANO_EUNSUPPORTED;
     if (q_ld >= (1ll << 38) || (long long)heads * pool->d > INT_MAX) return JANO_EUNSUPPORTED;
     if ((s = check_rows(q, q_ld, (long long)heads * pool->d)) != JANO_OK) return s;
     if ((s = check_rows(out, out_ld, (long long)heads * pool->d)) != JANO_OK) return s;

@@ -123,49 +123,59 @@ struct Plan {
     int seq, row0, rows0, rows1, seen;   // rows of the two tiles, keys that any of them sees; rows0 = 0: nothing
 };
 
+// A sequence's rows and length, and its query tile pairs (0: none, or a bad one).
+struct SeqRows {
+    int lo, hi, len, tiles;
+};
+__device__ __forceinline__ SeqRows seq_rows(const Args& a, int s, bool report) {
+    SeqRows q{0, 0, 0, 0};
+    if (s >= a.n_seqs) return q;
+    q.lo = __ldg(a.cu + s);
+    q.hi = __ldg(a.cu + s + 1);
+    q.len = __ldg(a.lens + s);
+    const bool ok = q.lo >= 0 && q.lo <= q.hi && q.hi <= a.n_rows && q.hi - q.lo <= a.max_rows && q.len >= 0 &&
+                    q.len <= a.max_len && (s > 0 || q.lo == 0);
+    if (!ok && report) raise_error(a.err, JANO_EINDEX);
+    const int step = 2 * a.tile_rows;
+    if (ok) q.tiles = (q.hi - q.lo + step - 1) / step;
+    return q;
+}
+
 // The x-th query tile pair of all sequences.  The longest of every 32
 // sequences come first, so that the last CTAs to start are short ones, and the
 // later tiles of a sequence before its earlier ones: under causal limits they
 // see the most keys.
 __device__ __forceinline__ Plan make_plan(const Args& a, int x, bool report) {
     const int lane = threadIdx.x & 31;
-    const int step = 2 * a.tile_rows;
     Plan p{0, 0, 0, 0, 0};
-    int done = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-        const int s = s0 + lane;
-        int lo = 0, hi = 0, len = 0, tiles = 0;
-        if (s < a.n_seqs) {
-            lo = __ldg(a.cu + s);
-            hi = __ldg(a.cu + s + 1);
-            len = __ldg(a.lens + s);
-            const bool ok = lo >= 0 && lo <= hi && hi <= a.n_rows && hi - lo <= a.max_rows && len >= 0 &&
-                            len <= a.max_len && (s > 0 || lo == 0);
-            if (!ok && report) raise_error(a.err, JANO_EINDEX);
-            tiles = ok ? (hi - lo + step - 1) / step : 0;
-        }
-        int before = 0;                            // tiles of the sequences that come first
-        const int others = min(32, a.n_seqs - s0);
-        for (int j = 0; j < others; ++j) {
-            const int l = __shfl_sync(0xFFFFFFFFu, len, j), t = __shfl_sync(0xFFFFFFFFu, tiles, j);
-            if (l > len || (l == len && j < lane)) before += t;
-        }
-        const bool mine = x >= done + before && x < done + before + tiles;
-        const unsigned who = __ballot_sync(0xFFFFFFFFu, mine);
-        if (who) {
-            const int src = __ffs(who) - 1;
-            const int t = tiles - 1 - (x - (done + before));
-            const int first = lo + t * step;
-            p.seq = s0 + src;
-            p.row0 = __shfl_sync(0xFFFFFFFFu, first, src);
-            const int left = __shfl_sync(0xFFFFFFFFu, hi - first, src);
-            p.rows0 = min(left, a.tile_rows);
-            p.rows1 = min(left - p.rows0, a.tile_rows);
-            p.seen = __shfl_sync(0xFFFFFFFFu, len, src);
-            break;
-        }
-        done += __reduce_add_sync(0xFFFFFFFFu, tiles);
+    SeqRows q;
+    int done = 0, s0 = 0;
+    for (;; s0 += 32) {
+        if (s0 >= a.n_seqs) return p;
+        q = seq_rows(a, s0 + lane, report);
+        const int all = __reduce_add_sync(0xFFFFFFFFu, q.tiles);
+        if (x < done + all) break;
+        done += all;
     }
+    int before = 0;                            // tiles of the sequences that come first
+    const int others = min(32, a.n_seqs - s0);
+    for (int j = 0; j < others; ++j) {
+        const int l = __shfl_sync(0xFFFFFFFFu, q.len, j), t = __shfl_sync(0xFFFFFFFFu, q.tiles, j);
+        if (l > q.len || (l == q.len && j < lane)) before += t;
+    }
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, x >= done + before && x < done + before + q.tiles);
+    if (who) {
+        const int src = __ffs(who) - 1;
+        const int first = q.lo + (q.tiles - 1 - (x - (done + before))) * 2 * a.tile_rows;
+        p.seq = s0 + src;
+        p.row0 = __shfl_sync(0xFFFFFFFFu, first, src);
+        const int left = __shfl_sync(0xFFFFFFFFu, q.hi - first, src);
+        p.rows0 = min(left, a.tile_rows);
+        p.rows1 = min(left - p.rows0, a.tile_rows);
+        p.seen = __shfl_sync(0xFFFFFFFFu, q.len, src);
+    }
+    if (report)                                // the other sequences, for their errors
+        for (int s = s0 + 32 + lane; s < a.n_seqs; s += 32) seq_rows(a, s, true);
     if (a.limits && p.rows0 > 0) {
         int most = 0;
         for (int i = lane; i < p.rows0 + p.rows1; i += 32) most = max(most, __ldg(a.limits + p.row0 + i));

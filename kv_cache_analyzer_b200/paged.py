@@ -286,7 +286,7 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_rows, out=None
     if max_rows is None:
         max_rows = n
     if max_len is None:
-        max_len = page_table.shape[1] * page_size
+        max_len = min(page_table.shape[1] * page_size, 1 << 26)          # the longest that a call takes
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws, ws_bytes = _list(workspace, "workspace", workspace.numel(), dev, torch.uint8), workspace.numel()

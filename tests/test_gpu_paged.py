@@ -239,6 +239,24 @@ def test_few_rows_match_oracle(J, rows, lens, heads, kv_heads, d, page, kind, op
     assert all(torch.equal(o, outs[0]) for o in outs)             # the same sums in the same order
 
 
+@pytest.mark.parametrize("split", [0, 1, 2])
+def test_a_bad_sequence_late_in_a_long_list_is_reported(J, split):
+    n = 300                                             # sequences; the 128-at-a-time search crosses three groups
+    p = Paged([1 + s % 2 for s in range(n)], [(s * 37) % 150 + 1 for s in range(n)], 2, 1, 64, 16, seed=5)
+    want = attend(J, p, max_rows=2, split=split).clone()
+    no_device_error(J)
+    p.check(want)
+    lens = np.array(p.lens)
+    lens[283] = -1
+    out = torch.full_like(p.dev_q, 3.0)
+    J.paged_attention(p.dev_q, p.dev_k, p.dev_v, p.dev_table, ints(lens), p.dev_cu, out=out, max_rows=2, split=split)
+    assert J.device_error() == 6
+    bad = slice(int(p.cu[283]), int(p.cu[284]))
+    assert bool((out[bad] == 3.0).all())
+    out[bad] = want[bad]
+    p.check(out)
+
+
 def test_few_rows_report_bad_lists_and_need_their_workspace(J):
     p = Paged([1, 2], [100, 200], 2, 2, 64, 16, seed=12)
     out = torch.full_like(p.dev_q, 3.0)

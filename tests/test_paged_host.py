@@ -132,6 +132,7 @@ def test_paged_attention_refusals(J):
         return L.jano_paged_attention(p or pool(J), s or seqs(J), q, q_ld, nil, n, max_rows, max_len, heads, scale, split,
                                       ws, 0, out, o_ld, nil)
     assert call(n=0, q=nil) == 0 and call(n=-1) == EINVAL and call(max_len=-1) == EINVAL and call(max_rows=-1) == EINVAL
+    assert call(max_len=2 ** 26 + 1) == EUNSUPPORTED
     for kw, code in POOLS:
         assert call(p=pool(J, **kw)) == code, kw
     for kw, code in SEQS:
