@@ -1,4 +1,4 @@
-"""Several generations over one page pool: the cache step of a layer for a
+"""Several generations over one page pool: the cache step of each layer for a
 batch of images and videos of different sizes.
 
 A generation keeps its whole sequence cached and refreshes only its due tokens
@@ -39,21 +39,31 @@ class BatchPlan:
 
 class PagedBatch:
     """Page pool of `n_pages` pages of `page_size` tokens, shared by the open
-    generations.  heads query heads attend over kv_heads K/V heads of size d;
-    with a rope, K and Q are rotated by their token's position (on the rope's
-    grid, or on each generation's own, see ``open``)."""
+    generations: K and V pages per layer, one page table for all layers.  heads
+    query heads attend over kv_heads K/V heads of size d; with a rope, K and Q
+    are rotated by their token's position (on the rope's grid, or on each
+    generation's own, see ``open``).  All work is launched on `stream`."""
 
     def __init__(self, *, n_pages: int, page_size: int, heads: int, d: int, kv_heads: int | None = None,
-                 rope: Rope | None = None, head_major: bool = False, device="cuda", stream=None):
+                 rope: Rope | None = None, layers: int = 1, head_major: bool = False, device="cuda", stream=None):
         self.page_size, self.heads, self.d = page_size, heads, d
         self.kv_heads = heads if kv_heads is None else kv_heads
         self.dev, self.stream = torch.device(device), stream
-        self.k_pages, self.v_pages = page_pool(n_pages, page_size, self.kv_heads, d, head_major, self.dev)
+        if layers < 1:
+            raise ValueError(f"layers must be at least 1, got {layers}")
+        with self._on_stream():
+            self.layers = [page_pool(n_pages, page_size, self.kv_heads, d, head_major, self.dev)
+                           for _ in range(layers)]
+        self.k_pages, self.v_pages = self.layers[0]
         self.rope = rope
         self.table = None if rope is None else rope_table(rope, stream=stream)
         self._free = list(range(n_pages))[::-1]
         self._gens: dict[int, dict] = {}
         self._next = 0
+
+    def _on_stream(self):
+        """Memory made here belongs to the batch's stream: it is reused behind the steps that read it."""
+        return contextlib.nullcontext() if self.stream is None else torch.cuda.stream(_torch_stream(self.stream))
 
     # ------------------------------------------------------------------ pages
     @property
@@ -113,15 +123,13 @@ class PagedBatch:
         grids = None
         if self.rope is not None and any(g["grid"] is not None for g in gens):
             grids = torch.tensor([g["grid"] or self.rope.grid for g in gens], dtype=torch.int32)
-        # made on the batch's stream: a dropped plan's memory is reused there, behind the steps that read it
-        on = contextlib.nullcontext() if self.stream is None else torch.cuda.stream(_torch_stream(self.stream))
-        with on:
+        with self._on_stream():
             lists = dict(page_table=table.to(self.dev), seq_lens=lens.to(self.dev), cu_rows=cu.to(self.dev))
             grids = None if grids is None else grids.to(self.dev)
         return BatchPlan(lists, grids, max(counts), int(lens.max()), sum(counts),
                          tuple((gen, g["tokens"]) for (gen, _), g in zip(rows, gens)))
 
-    def step(self, plan: BatchPlan, q, k, v, pos, limits=None, out=None):
+    def step(self, plan: BatchPlan, q, k, v, pos, limits=None, out=None, layer: int = 0):
         """One layer's step of a planned batch: k, v [rows][kv_heads][d] of
         the due tokens pos (int32, rising within a generation) go to their
         pages, q [rows][heads][d] attends.  limits: positions each row sees
@@ -131,7 +139,8 @@ class PagedBatch:
                 raise ValueError(f"generation {gen} grew or closed after the plan was made")
         if pos.numel() != plan.n_rows:
             raise ValueError(f"the plan has {plan.n_rows} rows, got {pos.numel()}")
-        q_rot = paged_append(k, v, pos, self.k_pages, self.v_pages, **plan.lists, rope=self.rope, table=self.table,
+        k_pages, v_pages = self.layers[layer]
+        q_rot = paged_append(k, v, pos, k_pages, v_pages, **plan.lists, rope=self.rope, table=self.table,
                              q=q, grids=plan.grids, stream=self.stream)
-        return paged_attention(q_rot, self.k_pages, self.v_pages, **plan.lists, limits=limits, out=out,
+        return paged_attention(q_rot, k_pages, v_pages, **plan.lists, limits=limits, out=out,
                                max_rows=plan.max_rows, max_len=plan.max_len, stream=self.stream)

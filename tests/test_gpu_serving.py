@@ -101,6 +101,27 @@ def test_streamed_generation_grows_frame_by_frame(J):
         check_attention(out, qr[sl], kr[:last * per], f64(v[:last * per]), limits, d ** -0.5)
 
 
+def test_layers_keep_their_own_pages(J):
+    from kv_cache_analyzer_b200.serving import PagedBatch
+    b = PagedBatch(n_pages=8, page_size=16, heads=2, d=64, layers=2)
+    one = PagedBatch(n_pages=8, page_size=16, heads=2, d=64)
+    g, h = b.open(90), one.open(90)
+    pos = ints(np.arange(90))
+    plan, alone = b.plan([(g, 90)]), one.plan([(h, 90)])
+    rows = [[synth.normal_bf16((90, 2, 64), seed=3 * layer + s).cuda() for s in range(3)] for layer in range(2)]
+    outs = [b.step(plan, *rows[layer], pos, layer=layer) for layer in range(2)]
+    for layer in range(2):                                 # without a rope: the rows as they are
+        assert torch.equal(one.step(alone, *rows[layer], pos), outs[layer])
+    # a second step of layer 0 still finds its own keys
+    few = b.plan([(g, 1)])
+    q, k, v = (x[:1].contiguous() for x in rows[0])
+    got = b.step(few, q, k, v, ints([0]))
+    assert J.device_error() == 0
+    check_attention(got, f64(q), f64(rows[0][1]), f64(rows[0][2]), np.array([90]), 64 ** -0.5)
+    with pytest.raises(IndexError):
+        b.step(few, q, k, v, ints([0]), layer=2)
+
+
 def test_batch_step_replays_as_a_graph_on_a_side_stream(J):
     from kv_cache_analyzer_b200.serving import PagedBatch
     s = torch.cuda.Stream()
