@@ -588,7 +588,7 @@ JANO_API jano_status jano_paged_append(const jano_page_pool *pool, const jano_pa
  * workspace  device scratch of ws_bytes >= jano_paged_attention_workspace_bytes
  *          bytes, 16-byte aligned, or NULL.  With n_split = 0 and few rows per
  *          sequence (the query's bytes are not 0) it selects the form for
- *          them: every SM takes an equal share of all key tiles, whatever the
+ *          them: every SM takes a share of all key tiles, whatever the
  *          lengths, and the partials at the shares' ends go through it.  Its
  *          contents are overwritten and need no zeroing; calls that may
  *          overlap need workspaces of their own.

@@ -354,8 +354,8 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
                 }
             }
             Feed<HD, false> feed{ctl, is_v ? &tmV : &tmK, is_v ? L::bFullV : L::bFullK,
-                                            is_v ? L::bEmptyV : L::bEmptyK, L::bLand, is_v,
-                                            base + (is_v ? L::kRingV : L::kRingK), RingPos(L::kSlots)};
+                                 is_v ? L::bEmptyV : L::bEmptyK, L::bLand, is_v,
+                                 base + (is_v ? L::kRingV : L::kRingK), RingPos(L::kSlots)};
             feed.tiles(a.table + (long long)seq * a.max_pages, a.page_shift, a.n_pages, kt0, n, seen, head);
             if (!is_v) ptx::mbar_wait(ctl.bar(L::bQFull), 0, kWaitLimit);
             feed.drain();
