@@ -177,7 +177,8 @@ def axis_rope(x, rope: Rope, table, ids=None, coords=None, out=None, stream=None
         out = _new(stream, (n, h, d), x)
     o_ptr, o_ld = _rows(out, "out", dev, n, h, d)
     jano_axis_rope(x_ptr, x_ld, _list(ids, "ids", n, dev), _list(coords, "coords", 3 * n, dev), n, h, d,
-                   rope.packed(), _list(table, "table", 2 * rope.entries, dev, _F32), o_ptr, o_ld, _launch_stream(stream, dev))
+                   rope.packed(), _list(table, "table", 2 * rope.entries, dev, _F32), o_ptr, o_ld,
+                   _launch_stream(stream, dev))
     return out
 
 
@@ -270,7 +271,9 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_rows, out=None
     form: give max_rows where it is small); split: CTAs that share one query
     tile's keys (0: the library's choice).  workspace: a device uint8 tensor
     of jano_paged_attention_workspace_bytes bytes, allocated here if None and
-    needed.  Rows past cu_rows[-1] of out are left as they are."""
+    needed; calls that may overlap (streams, captured graphs) must not share
+    one.  K and V below a sequence's length must be finite.  Rows past
+    cu_rows[-1] of out are left as they are."""
     n, h, d = _shape3(q, "q")
     dev = _device(q, "q")
     q_ptr, q_ld = _rows(q, "q", dev, n, h, d)
@@ -297,5 +300,6 @@ def paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_rows, out=None
             ws = workspace.data_ptr()
     jano_paged_attention(pool, _seqs(page_table, seq_lens, cu_rows, dev), q_ptr, q_ld,
                          _list(limits, "limits", n, dev), n, max_rows, max_len, h,
-                         d ** -0.5 if scale is None else scale, split, ws, ws_bytes, o_ptr, o_ld, _launch_stream(stream, dev))
+                         d ** -0.5 if scale is None else scale, split, ws, ws_bytes, o_ptr, o_ld,
+                         _launch_stream(stream, dev))
     return out
