@@ -60,12 +60,13 @@ def _list(t: torch.Tensor | None, name: str, n: int, dev: int, dtype=_I32) -> in
 
 def _rows(t: torch.Tensor, name: str, dev: int, n: int, heads: int, d: int) -> tuple:
     """(address, row distance) of rows [n][heads][d]."""
-    shape, strides = t.shape, t.stride()
-    if (t.dtype is not _BF16 or t.get_device() != dev or shape != (n, heads, d) or (strides[2] != 1 and d > 1) or
-            (strides[1] != d and heads > 1)):
-        raise _wrong(t, name, dev, _BF16, f"[{n}][{heads}][{d}], its heads and columns adjacent")
-    # one row lies at any distance from the next: the least that the call takes
-    return t.data_ptr(), strides[0] if n > 1 else -(-heads * d // 8) * 8
+    if t.dtype is _BF16 and t.get_device() == dev and t.shape == (n, heads, d):
+        if t.is_contiguous():                  # (a single row too, whatever its stride)
+            return t.data_ptr(), heads * d
+        strides = t.stride()
+        if (strides[2] == 1 or d == 1) and (strides[1] == d or heads == 1):
+            return t.data_ptr(), strides[0] if n > 1 else heads * d
+    raise _wrong(t, name, dev, _BF16, f"[{n}][{heads}][{d}], its heads and columns adjacent")
 
 
 def _shape3(t: torch.Tensor, name: str) -> tuple:
@@ -114,7 +115,7 @@ def _seqs(page_table: torch.Tensor, seq_lens: torch.Tensor, cu_rows: torch.Tenso
 
 
 # ---------------------------------------------------------------- rotary positions
-@dataclass(frozen=True)
+@dataclass(frozen=True, init=False)
 class Rope:
     """Rotary positions with up to three axes (frame, row, column).
 
@@ -131,11 +132,13 @@ class Rope:
     pairing: str = "interleaved"
     shared: bool = False
 
-    def __post_init__(self):
-        if self.pairing not in ("interleaved", "halves"):
-            raise ValueError(f"pairing must be 'interleaved' or 'halves', got {self.pairing!r}")
-        if len(self.axes) != 3 or len(self.n_pos) != 3 or len(self.grid) != 2:
+    def __init__(self, axes, n_pos, grid=(0, 0), theta=10000.0, pairing="interleaved", shared=False):
+        if pairing not in ("interleaved", "halves"):
+            raise ValueError(f"pairing must be 'interleaved' or 'halves', got {pairing!r}")
+        if len(axes) != 3 or len(n_pos) != 3 or len(grid) != 2:
             raise ValueError("axes and n_pos have three entries, grid has two")
+        # past the frozen class's __setattr__: 0.7 us, not 1.2 (a call of few rows costs the host 12)
+        self.__dict__.update(axes=axes, n_pos=n_pos, grid=grid, theta=theta, pairing=pairing, shared=shared)
 
     @classmethod
     def of(cls, geom: Geometry, axes, **kw) -> "Rope":
@@ -251,7 +254,8 @@ def paged_append(k, v, pos, k_pages, v_pages, page_table, seq_lens, cu_rows, rop
     q_ptr, q_ld, o_ptr, o_ld, heads, q_out = _queries(q, q_out, n, d, dev, stream)
     jano_paged_append(_pool(k_pages, v_pages, dev), seqs, q_ptr, q_ld, k_ptr, k_ld, v_ptr, v_ld,
                       _list(pos, "pos", n, dev), _list(coords, "coords", 3 * n, dev),
-                      _list(grids, "grids", 2 * page_table.shape[0], dev), n, heads, cfg, table, o_ptr, o_ld,
+                      None if grids is None else _list(grids, "grids", 2 * page_table.shape[0], dev), n, heads, cfg,
+                      table, o_ptr, o_ld,
                       _launch_stream(stream, dev))
     return q_out
 
