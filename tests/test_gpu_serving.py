@@ -206,3 +206,39 @@ def test_hot_path_with_a_rope_equals_its_parts(J):
     stream.synchronize()
     assert torch.equal(hp.out[idx.long()], first[idx.long()])
     del g
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_calls_in_a_row_see_what_the_ones_before_wrote(J, rows):
+    # each kernel sets itself up while the one in front ends: a chain in which every call reads the last
+    # one's output (rows, lengths, cache) gives bit for bit what it gives with a wait after every call
+    from kv_cache_analyzer_b200.serving import PagedBatch
+    rope = J.Rope(axes=(16, 24, 24), n_pos=(8, 16, 16), grid=(16, 16))
+    start = synth.normal_bf16((rows, 4, 64), seed=1).cuda()
+
+    def chain(wait):
+        b = PagedBatch(n_pages=80, page_size=16, heads=4, d=64, rope=rope)
+        g = b.open(1200)
+        b.k_pages.fill_(0.25)
+        b.v_pages.fill_(0.5)
+        plan = b.plan([(g, rows)])
+        x, outs = start.clone(), []
+        for i in range(60):
+            pos = torch.arange(i * 7, i * 7 + rows, device="cuda", dtype=torch.int32)
+            plan.lists["seq_lens"].fill_(100 + 17 * i)             # written by a kernel in front
+            if wait:
+                torch.cuda.synchronize()
+            y = J.axis_rope(x, rope, b.table, ids=pos)
+            if wait:
+                torch.cuda.synchronize()
+            x = b.step(plan, y, x, y, pos, limits=pos + 60)
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(x)
+        torch.cuda.synchronize()
+        assert J.device_error() == 0
+        return torch.stack(outs)
+
+    want = chain(True)
+    for _ in range(5):
+        assert torch.equal(chain(False), want)
