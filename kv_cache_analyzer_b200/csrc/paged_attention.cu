@@ -490,9 +490,10 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
         const int steps = single ? (n + 1 - i) >> 1 : n;
         // the stream's tiles start at keys first, first + apart, ...
         const int first = (kt0 + (single ? i : 0)) * BN, apart = single ? 2 * BN : BN;
+        // (0 for any limit below it: what follows subtracts key positions from it)
         int limit = seen;
         if (a.limits && row < (i && !single ? rows1 : rows0) * a.group)
-            limit = min(seen, __ldg(a.limits + row0 + (i && !single ? a.tile_rows : 0) + row / a.group));
+            limit = max(0, min(seen, __ldg(a.limits + row0 + (i && !single ? a.tile_rows : 0) + row / a.group)));
         // steps whose tile every row of the warp sees whole; the rest is masked
         const int whole = __reduce_min_sync(0xFFFFFFFFu, limit) - first - BN;
         const int plain = whole < 0 ? 0 : min(steps, whole / apart + 1);

@@ -563,8 +563,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const bool live = lane < s.rows * a.group;
             const int first = (s.kt0 + st) * BN;
             const int row = s.row0 + lane / a.group;
+            // (0 for any limit below it: what follows subtracts key positions from it)
             int limit = s.seen;
-            if (a.limits && live) limit = min(s.seen, __ldg(a.limits + row));
+            if (a.limits && live) limit = max(0, min(s.seen, __ldg(a.limits + row)));
             // steps whose tile every row sees whole; the rest is masked
             const int whole = __reduce_min_sync(0xFFFFFFFFu, limit) - first - BN;
             const int plain = whole < 0 ? 0 : min(steps, whole / (2 * BN) + 1);
