@@ -98,8 +98,9 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int n_seqs, int r) 
 }
 
 // Coordinates, cache base and validity of a row; false: the row is skipped.
-__device__ __forceinline__ bool resolve(const Args& a, int r, int t, int t_before, bool want_coords, int (&p)[3],
-                                        long long& base) {
+// The same for each of a row's tensors, those that are not rotated among them:
+// a row is written whole or not at all.
+__device__ __forceinline__ bool resolve(const Args& a, int r, int t, int t_before, int (&p)[3], long long& base) {
     const Place& w = a.at;
     int seq = 0;
     int first = 0;
@@ -123,7 +124,7 @@ __device__ __forceinline__ bool resolve(const Args& a, int r, int t, int t_befor
         bad = bad || t >= w.n_tokens;
         base = (long long)t * w.token_stride;
     }
-    if (!bad && want_coords) {
+    if (!bad && a.tab.slots > 0) {                         // (0: a call without a rotation)
         if (w.coords) {
             p[0] = __ldg(w.coords + 3ll * r);
             p[1] = __ldg(w.coords + 3ll * r + 1);
@@ -265,7 +266,7 @@ rope_rows_kernel(const __grid_constant__ Args a) {
 
     int p[3] = {0, 0, 0};
     long long base = 0;
-    if (!resolve(a, r, id, id_before, rot, p, base)) return;
+    if (!resolve(a, r, id, id_before, p, base)) return;
     uint4* dst = jb.dst + (jb.cached ? base : (long long)r * jb.dst_ld);
     float c[kN], s[kN];
     if (kFixed && rot) load_cs<kN>(a.tab, p, my_unit * kN, c, s);
