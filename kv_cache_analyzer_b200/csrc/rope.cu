@@ -92,7 +92,8 @@ __device__ __forceinline__ int seq_of_row(const int32_t* cu, int n_seqs, int r) 
         if (step == 1) break;
     }
     const int a = __ldg(cu + lo), b = __ldg(cu + lo + 1);
-    if (a <= r && r < b) return a == 0 || (a > 0 && lo > 0) ? lo : -2;
+    // (a sequence that begins at 0 behind others: these must be without rows)
+    if (a <= r && r < b) return a > 0 ? (lo > 0 ? lo : -2) : (a == 0 && (lo == 0 || __ldg(cu) == 0) ? lo : -2);
     // behind the last sequence: the search ends there, and it ends before r
     return lo == n_seqs - 1 && a <= b && b <= r && __ldg(cu) == 0 ? -1 : -2;
 }

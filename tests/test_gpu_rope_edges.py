@@ -116,3 +116,19 @@ def test_append_without_a_rope_has_no_coordinates_to_check(J):
     J.paged_append(k, k, ints(range(6)), kp, vp, ints([[1]]), ints([6]), ints([0, 6]))
     assert J.device_error() == 0
     assert torch.equal(kp[1, :6], k) and torch.equal(vp[1, :6], k)
+
+
+@pytest.mark.parametrize("cu", [[-3, 0, 4], [-1, 0, 0, 4], [-2 ** 31, 0, 4]])
+def test_append_reports_a_row_list_that_does_not_begin_at_zero(J, cu):
+    # the rows lie in a later sequence, whose own bounds are good
+    k = synth.normal_bf16((4, 2, 64), seed=1).cuda()
+    kp, vp = (torch.full((8, 16, 2, 64), 100.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    n = len(cu) - 1
+    q_out = torch.full_like(k, 100.0)
+    J.paged_append(k, k, ints(range(4)), kp, vp, ints(np.arange(n)[:, None]), ints([4] * n), ints(cu), q=k, q_out=q_out)
+    assert J.device_error() == EINDEX
+    assert not changed(kp, 100.0).any() and not changed(vp, 100.0).any() and not changed(q_out, 100.0).any()
+    # sequences without rows in front of it are no fault
+    J.paged_append(k, k, ints(range(4)), kp, vp, ints([[0], [1], [2]]), ints([4, 4, 4]), ints([0, 0, 0, 4]))
+    assert J.device_error() == 0
+    assert torch.equal(kp[2, :4], k) and torch.equal(vp[2, :4], k)
