@@ -181,9 +181,15 @@ struct Shares {
 // item drains and fills its pipeline in between, as long as three tiles take
 // (one token of 24 heads over 4,096 tokens: the CTAs that cross ended after 15
 // to 17 us, the others after 12 to 14; 21.3 us in all, 19.3 without crossing).
-// Parts of an item of `tiles` (a float quotient: what this computes counts).
+// Parts of an item of `tiles`: tiles / quota, rounded up.  The float quotient
+// (what this computes counts: integer divisions cost 1 us of start) is only an
+// estimate, off by one at most up to 2^19 tiles; what is left over corrects it,
+// so that the attention and the merge kernel cut an item alike however each is
+// compiled.
 __device__ __forceinline__ int item_parts(int tiles, int quota) {
-    return min(tiles, max(1, (int)ceilf(__fdividef((float)tiles, (float)quota) - 0.001f)));
+    const int q = (int)__fdividef((float)tiles, (float)quota);
+    const int left = tiles - q * quota;
+    return q + (left > 0) + (left > quota) - (left <= -quota);
 }
 // The quota, 0 for equal shares.  The whole warp; n_seqs <= 32, `tiles` the lane's sequence's.
 __device__ __forceinline__ int item_quota(const Args& a, int tiles, const Shares& sh, int ctas) {

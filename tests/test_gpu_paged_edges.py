@@ -62,3 +62,39 @@ def test_limits_down_to_the_lowest_int(J, rows, lens, heads, kv_heads, splits, d
             attend(J, p, limits, out=out, **kw)
             no_device_error(J)
             p.check(out, limits)
+
+
+@pytest.mark.parametrize("tiles", [73999, 74000, 74001])
+def test_few_rows_of_two_items_cut_at_a_thousand_tiles(J, tiles):
+    # Parts of some thousand key tiles, one tile less and more than a multiple: every part must be found again
+    # by the merge.  The sequences go through 64 pages one after another, and page c has its V in column c
+    # alone, so column c is the weight of a 64th of the keys: a lost or doubled part (a 74th) shows there.
+    gen = np.random.default_rng(tiles)
+    lens = [tiles * 128, 73556 * 128]
+    page, d, n_pages = 256, 64, 64
+    per = [-(-m // page) for m in lens]
+    table = np.zeros((2, max(per)), dtype=np.int64)
+    for s in range(2):
+        table[s, :per[s]] = np.arange(per[s]) * n_pages // per[s]
+    k = torch.from_numpy(gen.standard_normal((n_pages, page, 1, d))).bfloat16()
+    v = torch.zeros_like(k)
+    for c in range(n_pages):
+        v[c, :, 0, c] = 1.0
+    q = torch.from_numpy(gen.standard_normal((2, 1, d))).bfloat16()
+    out = J.paged_attention(q.cuda(), k.cuda(), v.cuda(), ints(table), ints(lens), ints([0, 1, 2]), max_rows=1)
+    no_device_error(J)
+    for s in range(2):
+        times = np.bincount(table[s, :per[s]], minlength=n_pages).astype(np.float64)[:, None] * np.ones(page)
+        last = per[s] * page - lens[s]                               # places of the last page past the length
+        if last:
+            times[table[s, per[s] - 1], page - last:] -= 1.0
+        kk, qq = k[:, :, 0].double().numpy(), q[s, 0].double().numpy()
+        z = kk @ qq * d ** -0.5
+        w = times * np.exp(z - z.max())
+        want = w.sum(1) / w.sum()
+        top = (np.abs(kk) @ np.abs(qq)).max() * d ** -0.5
+        # as check_attention, and the fp32 sums of a share's O: 8 additions a tile, each off by at most 2^-23
+        bound = (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -15 * top + 2.0 ** -12 + 8 * 1002 * 2.0 ** -23) * want
+        err = np.abs(out[s, 0].double().cpu().numpy() - want)
+        assert np.all(err <= bound), (s, float((err / want).max()), float((bound / want).max()))
+        assert float((bound / want).max()) < 0.5 * 64 / 75            # below what half of a part would move
