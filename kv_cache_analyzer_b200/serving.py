@@ -18,6 +18,7 @@ as the graph, and capture again once one of its generations grew or closed).
 from __future__ import annotations
 
 import contextlib
+import operator
 from dataclasses import dataclass
 
 import torch
@@ -75,21 +76,25 @@ class PagedBatch:
         reserved now; their contents are whatever the pages held until they
         are appended).  grid: its (rows, columns) of tokens, if it differs from
         the rope's."""
+        g = dict(pages=[], tokens=0, grid=grid)
+        # (before the batch knows of it: a refused generation leaves nothing)
+        self._reserve(g, operator.index(n_tokens))
         gen = self._next
         self._next += 1
-        self._gens[gen] = dict(pages=[], tokens=0, grid=grid)
-        try:
-            self.extend(gen, n_tokens)
-        except RuntimeError:
-            del self._gens[gen]
-            raise
+        self._gens[gen] = g
         return gen
 
     def extend(self, gen: int, n_tokens: int) -> None:
         """The generation grows to n_tokens cached positions."""
         g = self._gens[gen]
+        n_tokens = operator.index(n_tokens)
         if n_tokens < g["tokens"]:
             raise ValueError(f"generation {gen} has {g['tokens']} tokens, cannot shrink to {n_tokens}")
+        self._reserve(g, n_tokens)
+
+    def _reserve(self, g: dict, n_tokens: int) -> None:
+        if n_tokens < 0:
+            raise ValueError(f"a generation cannot have {n_tokens} tokens")
         need = -(-n_tokens // self.page_size) - len(g["pages"])
         if need > len(self._free):
             raise RuntimeError(f"page pool exhausted: {need} pages needed, {len(self._free)} free")

@@ -1,0 +1,35 @@
+"""PagedBatch's bookkeeping of generations on the host.  No GPU is needed."""
+import numpy as np
+import pytest
+
+from kv_cache_analyzer_b200.serving import PagedBatch
+
+
+@pytest.fixture
+def batch():
+    return PagedBatch(n_pages=10, page_size=16, heads=4, kv_heads=2, d=64, device="cpu")
+
+
+@pytest.mark.parametrize("n,error", [(-1, ValueError), (161, RuntimeError), (2.5, TypeError), (32.0, TypeError),
+                                     ("32", TypeError), (None, TypeError), (float("nan"), TypeError)])
+def test_a_refused_generation_leaves_nothing_behind(batch, n, error):
+    kept = batch.open(20)
+    state = dict(batch._gens[kept], pages=list(batch._gens[kept]["pages"]))
+    free = list(batch._free)
+    with pytest.raises(error):
+        batch.open(n)
+    assert list(batch._gens) == [kept] and batch._free == free
+    # and a refused growth leaves the generation as it was
+    with pytest.raises(error):
+        batch.extend(kept, n)
+    assert batch._gens[kept] == state and batch._free == free
+    with pytest.raises(KeyError):
+        batch.extend(kept + 1, 40)
+    assert batch.open(32) != kept and batch.free_pages == 10 - 2 - 2
+
+
+def test_token_counts_may_be_numpy_integers(batch):
+    g = batch.open(np.int64(33))
+    batch.extend(g, np.int32(49))
+    assert batch.free_pages == 6
+    assert batch.plan([(g, 3)]).lists["seq_lens"].tolist() == [49]
