@@ -160,11 +160,14 @@ class Rope:
         return x * (a // 2) + y * (b // 2) + z * (c // 2)
 
 
-def rope_table(rope: Rope, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+def rope_table(rope: Rope, out: torch.Tensor | None = None, stream=None, device="cuda") -> torch.Tensor:
     """The (cos, sin) table of a rotation, fp32 [entries][2]: axis 0's
-    positions x slots, then axis 1's, then axis 2's."""
+    positions x slots, then axis 1's, then axis 2's.  Without out it is made
+    on `device` (default: the current one), on its stream `stream`."""
     if out is None:
-        out = _new(stream, (rope.entries, 2), torch.empty(0, dtype=_F32, device="cuda"))
+        with torch.cuda.device(device):
+            out = _new(stream, (rope.entries, 2), torch.empty(0, dtype=_F32, device="cuda"))
+            return rope_table(rope, out, stream)
     _list(out, "out", 2 * rope.entries, _device(out, "out"), _F32)
     jano_rope_table(rope.c(), rope.theta, int(rope.shared), out, stream)
     return out

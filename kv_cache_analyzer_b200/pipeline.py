@@ -63,7 +63,7 @@ class HotPath:
         self.q_act = self.k_act = self.v_act = self.q_rot = None
         # with a rope, q_act and k_act hold the unrotated rows and stay as they are
         self.rope = rope
-        self.rope_table = None if rope is None else rope_table(rope, stream=self.stream)
+        self.rope_table = None if rope is None else rope_table(rope, stream=self.stream, device=self.dev)
         self.host_offsets = None
         self._lgc, self._tgc, self._sc = lg.c(), token_geom.c(), sched.c()
 

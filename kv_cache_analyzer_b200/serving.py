@@ -57,7 +57,7 @@ class PagedBatch:
                            for _ in range(layers)]
         self.k_pages, self.v_pages = self.layers[0]
         self.rope = rope
-        self.table = None if rope is None else rope_table(rope, stream=stream)
+        self.table = None if rope is None else rope_table(rope, stream=stream, device=self.dev)
         self._free = list(range(n_pages))[::-1]
         self._gens: dict[int, dict] = {}
         self._next = 0

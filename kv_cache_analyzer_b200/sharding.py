@@ -125,7 +125,7 @@ class ShardedHotPath:
         self.last_split = 1
         self.q_act = self.k_act = self.v_act = self.q_rot = None
         self.rope = rope
-        self.rope_table = None if rope is None else rope_table(rope, stream=self.stream)
+        self.rope_table = None if rope is None else rope_table(rope, stream=self.stream, device=self.dev)
         self.host_offsets = None
         self._sgc, self._tgc, self._sc = self.slab_geom.c(), token_geom.c(), sched.c()
 

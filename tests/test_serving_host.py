@@ -1,7 +1,11 @@
 """PagedBatch's bookkeeping of generations on the host.  No GPU is needed."""
+import contextlib
+
 import numpy as np
 import pytest
+import torch
 
+import kv_cache_analyzer_b200.paged as P
 from kv_cache_analyzer_b200.serving import PagedBatch
 
 
@@ -33,3 +37,32 @@ def test_token_counts_may_be_numpy_integers(batch):
     batch.extend(g, np.int32(49))
     assert batch.free_pages == 6
     assert batch.plan([(g, 3)]).lists["seq_lens"].tolist() == [49]
+
+
+def test_a_rotations_table_is_made_on_the_batchs_device(monkeypatch):
+    # (another device than the current one: pools and table have to meet in one call)
+    rope = P.Rope(axes=(16, 24, 24), n_pos=(2, 5, 7), grid=(5, 7))
+    inside, seen = [], []
+
+    @contextlib.contextmanager
+    def on_device(device):
+        inside.append(torch.device(device))
+        yield
+        inside.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", on_device)
+    monkeypatch.setattr(P, "_new", lambda stream, shape, like: seen.append(("made", list(inside))) or torch.empty(shape))
+    monkeypatch.setattr(P, "_device", lambda t, name: -1)
+    monkeypatch.setattr(P, "jano_rope_table", lambda *a: seen.append(("filled", list(inside))))
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: empty(*a, **{**kw, "device": "cpu"}))
+    b = PagedBatch(n_pages=4, page_size=16, heads=4, d=64, rope=rope, device="cuda:3")
+    assert b.table.shape == (rope.entries, 2)
+    assert seen == [("made", [torch.device("cuda:3")]), ("filled", [torch.device("cuda:3")])]
+    seen.clear()
+    P.rope_table(rope, device="cuda:1")
+    assert seen == [("made", [torch.device("cuda:1")]), ("filled", [torch.device("cuda:1")])]
+    # a table that the caller brings stays where it is
+    seen.clear()
+    P.rope_table(rope, torch.zeros(rope.entries, 2))
+    assert seen == [("filled", [])]
