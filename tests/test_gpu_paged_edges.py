@@ -98,3 +98,86 @@ def test_few_rows_of_two_items_cut_at_a_thousand_tiles(J, tiles):
         err = np.abs(out[s, 0].double().cpu().numpy() - want)
         assert np.all(err <= bound), (s, float((err / want).max()), float((bound / want).max()))
         assert float((bound / want).max()) < 0.5 * 64 / 75            # below what half of a part would move
+
+
+@pytest.mark.parametrize("rows,n,heads,kv_heads,d,kw", [
+    ([130, 2], 640, 2, 2, 64, {}),                                      # a pair of tiles; some exponentials by polynomial
+    ([130, 2], 640, 2, 2, 64, dict(split=2)),
+    ([40, 1], 640, 2, 1, 64, dict(split=1)),                            # one tile, two streams of keys
+    ([40, 1], 1500, 2, 1, 128, dict(split=4)),
+    ([1, 2], 640, 2, 2, 64, dict(max_rows=2)),                          # few rows
+    ([2, 1], 2300, 2, 2, 128, dict(max_rows=2)),                        # ... an item in many parts
+    ([7, 9], 900, 3, 1, 64, dict(max_rows=9)),
+])
+def test_maxima_that_grow_in_every_form(J, rows, n, heads, kv_heads, d, kw):
+    # logits up to some hundreds that rise key by key (every tile makes the running maximum grow by more than the
+    # lazy rescale allows), fall (all but the first keys below the polynomial's clamp) and come in no order
+    for seed, order in enumerate((np.arange(n), np.arange(n)[::-1], np.random.default_rng(1).permutation(n))):
+        p = Paged(rows, [n, n], heads, kv_heads, d, 64, seed=seed)
+        scale_of = (0.25 * 2.0 ** (np.arange(n) * 6.4 / n))[order].astype(np.float32)
+        for s in range(2):
+            for j in range(n):
+                p.k[p.table[s, j // 64], j % 64] = p.q[0, :1] * float(scale_of[j])
+        p.dev_k = p.k.cuda()
+        out = attend(J, p, **kw)
+        no_device_error(J)
+        p.check(out)
+
+
+AT_SIZE = [  # rows, lengths, heads, kv_heads, d, page, limits ("token", a frame's tokens, or none)
+    ([4680], [32760], 12, 12, 128, 128, 1560),
+    ([16380], [32760], 12, 12, 128, 256, None),
+    ([1228, 1004, 0, 779], [4096, 3000, 2000, 3555], 24, 24, 128, 64, None),
+    ([4096], [16384], 24, 24, 64, 64, None),
+    ([2500, 700, 1, 40], [8192, 5000, 9000, 777], 24, 8, 64, 16, "token"),
+    ([2100, 3000], [8000, 3000], 10, 2, 128, 32, "token"),
+]
+
+
+@pytest.mark.parametrize("rows,lens,heads,kv_heads,d,page,mask", AT_SIZE)
+def test_long_chunks_at_size_on_sampled_rows(J, rows, lens, heads, kv_heads, d, page, mask):
+    # more CTAs than SMs, the library's split; sampled rows (the tiles' first and last ones among them) of every
+    # head against fp64 on the device
+    gen = torch.Generator("cuda").manual_seed(sum(rows))
+    n, per = sum(rows), [-(-m // page) for m in lens]
+    k, v = (torch.full((sum(per) + 1, page, kv_heads, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+            for _ in range(2))
+    order = torch.randperm(sum(per) + 1, generator=gen, device="cuda").int()
+    table = torch.full((len(rows), max(per)), 2 ** 30, dtype=torch.int32, device="cuda")
+    own = []
+    for s, m in enumerate(lens):
+        pages = order[sum(per[:s]):sum(per[:s + 1])]
+        table[s, :per[s]] = pages
+        kv = torch.randn((2, m, kv_heads, d), generator=gen, device="cuda").bfloat16()
+        at = torch.arange(m, device="cuda")
+        for t, x in zip((k, v), kv):
+            t[pages.long()[at // page], at % page] = x
+        own.append(kv)
+    q = torch.randn((n, heads, d), generator=gen, device="cuda").bfloat16()
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    pos = np.concatenate([np.arange(m - r, m) for r, m in zip(rows, lens)])
+    limits = None if mask is None else pos + 1 if mask == "token" else (pos // mask + 1) * mask
+    out = J.paged_attention(q, k, v, table, ints(lens), ints(cu), limits=None if limits is None else ints(limits))
+    no_device_error(J)
+    pick = np.random.default_rng(n)
+    step, g, scale = 128 // (heads // kv_heads), heads // kv_heads, d ** -0.5
+    for s, (r, m) in enumerate(zip(rows, lens)):
+        if not r:
+            continue
+        edges = np.arange(0, r, step)
+        take = np.unique(np.concatenate([pick.choice(edges, min(len(edges), 12), replace=False), pick.integers(0, r, 24),
+                                         [0, min(step, r) - 1, r - 1]]))
+        at = torch.from_numpy(cu[s] + take).cuda()
+        lim = torch.full((len(take),), m, device="cuda")
+        if limits is not None:
+            lim = torch.from_numpy(np.minimum(limits[cu[s] + take], m)).cuda()
+        hidden = torch.arange(m, device="cuda") >= lim[:, None]
+        for h in range(heads):
+            x, (kk, vv) = q[at, h].double(), own[s][:, :, h // g].double()
+            w = torch.softmax((x @ kk.T * scale).masked_fill_(hidden, -torch.inf), 1)
+            want, pv = w @ vv, w @ vv.abs()
+            top = (x.abs() @ kk.abs().T).masked_fill_(hidden, 0.0).amax(1, keepdim=True) * scale
+            # as check_attention, and the sums of O: 8 additions a key tile, each off by at most 2^-23
+            bound = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -15 * top + 2.0 ** -12 + m / 128 * 8 * 2.0 ** -23) * pv
+            over = (out[at, h].double() - want).abs() - bound
+            assert bool((over <= 0).all()), (s, h, float(over.max()), take[int(over.amax(1).argmax())])
