@@ -578,8 +578,8 @@ JANO_API jano_status jano_paged_append(const jano_page_pool *pool, const jano_pa
  * max_rows, max_len  upper bounds of a sequence's rows and length (grid and
  *          split choice only); a sequence above either, or with a bad length
  *          or cu_rows, raises JANO_EINDEX and its rows are not written.
- *          max_len at most 2^26 (JANO_EUNSUPPORTED): a bounded wait spans the
- *          keys of a CTA.
+ *          max_len at most 2^26 (JANO_EUNSUPPORTED): so far the bounds of the
+ *          waits that span a CTA's keys and the cut of a sequence hold.
  * n_split  CTAs that share one query tile's keys: 1, 2, 4 or 8 (a
  *          thread-block cluster), or 0 for the library's choice.
  * A page id outside the pool raises JANO_EINDEX and reads as zeros.  K and V

@@ -452,7 +452,7 @@ paged_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_con
       } else if (warp == 10 && ragged) {
         // ------------------------------------------------------------ V rows past the last key
         const int at = (n - 1) % L::kSlots;
-        if (ctl.warp_wait(L::bLand + at, 0)) {
+        if (ctl.warp_wait(L::bLand + at, 0, span_limit(n))) {
             const int live = seen - (nt - 1) * BN;
             uint8_t* v = gbase + L::kRingV + at * L::kTile;
             for (int e = live * 8 + lane; e < BN * 8; e += 32)

@@ -369,6 +369,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         a.part_ml[(2ll * blockIdx.x) * a.part_rows + lane] = make_float2(-INFINITY, -1.0f);
         a.part_ml[(2ll * blockIdx.x + 1) * a.part_rows + lane] = make_float2(-INFINITY, -1.0f);
     }
+    // warps that are ahead wait in the segments' ring for as long as one segment takes
+    const long long seg_limit = span_limit((a.max_len + BN - 1) / BN);
     // the planner and its first segment, while the others set up
     if (warp == 4) {
         Walk walk(a, blockIdx.x == 0);
@@ -381,7 +383,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         for (int q = 1; ok && more; ++q) {
             more = walk.next();
             const int k = q % kSegs;
-            ok = ctl.warp_poll(L::bSegEmpty + k, ((q / kSegs) & 1) ^ 1);
+            ok = ctl.warp_poll(L::bSegEmpty + k, ((q / kSegs) & 1) ^ 1, seg_limit);
             if (ok && lane == 0) {
                 ring[k] = walk.s;
                 ptx::mbar_arrive(ctl.bar(L::bSegFull + k));
@@ -415,14 +417,14 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
     // The q-th segment of this CTA, for one thread; false: a wait gave up.
     auto take = [&](int q, Seg& s) -> bool {
-        if (!ctl.poll(L::bSegFull + q % kSegs, (q / kSegs) & 1)) return false;
+        if (!ctl.poll(L::bSegFull + q % kSegs, (q / kSegs) & 1, seg_limit)) return false;
         s = ring[q % kSegs];
         ptx::mbar_arrive(ctl.bar(L::bSegEmpty + q % kSegs));
         return true;
     };
     // The same for a whole warp: every field the same in every lane.
     auto warp_take = [&](int q, Seg& s) -> bool {
-        if (!ctl.warp_poll(L::bSegFull + q % kSegs, (q / kSegs) & 1)) return false;
+        if (!ctl.warp_poll(L::bSegFull + q % kSegs, (q / kSegs) & 1, seg_limit)) return false;
         const Seg r = ring[q % kSegs];
         s.row0 = uniform(r.row0);
         s.rows = uniform(r.rows);
@@ -543,7 +545,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const int live = s.seen - (s.kt0 + s.n - 1) * BN;
             if (live >= BN) continue;
             const int at = (tiles - 1) % L::kSlots;    // the segment's last V
-            if (!ctl.warp_poll(L::bLand + at, (land_phase >> at) & 1u)) break;
+            if (!ctl.warp_poll(L::bLand + at, (land_phase >> at) & 1u, seg_limit)) break;
             land_phase ^= 1u << at;
             uint8_t* v = gbase + L::kRingV + at * L::kTile;
             for (int e = live * 8 + lane; e < BN * 8; e += 32)

@@ -17,7 +17,14 @@ namespace {
 constexpr int BM = 128;                      // rows of an MMA tile
 constexpr int BN = 128;                      // keys per tile
 constexpr uint32_t kPanel = 128 * 128;       // bytes of one 128-row x 64-column panel
-constexpr long long kWaitLimit = 1ll << 31;  // cycles (~1 s)
+#ifndef JANO_WAIT_CYCLES
+#define JANO_WAIT_CYCLES (1ll << 31)         // (test builds: shorter)
+#endif
+constexpr long long kWaitLimit = JANO_WAIT_CYCLES;   // ~1 s
+// A wait that spans key tiles, not the step of one: some more for each.  (A
+// tile takes up to 4,100 cycles, 2^26 keys in one CTA 1.1 s; where something
+// else failed, the abort flag ends the wait.)
+__device__ __forceinline__ long long span_limit(int tiles) { return kWaitLimit + (long long)tiles * 16384; }
 
 // Tensor memory of the two streams: S0 [0,128) S1 [128,256) O0 [256,256+d)
 // O1 [384,384+d); P_i, BF16, over the upper half of S_i.
@@ -33,25 +40,25 @@ struct Ctl {
     __device__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
     // Waiting threads sleep until the phase completes; the MMA warp polls
     // (its waits sit on every key tile's critical path).
-    __device__ bool wait(int i, uint32_t parity) const {
+    __device__ bool wait(int i, uint32_t parity, long long limit = kWaitLimit) const {
         if (ptx::mbar_try_wait_sleep(bar(i), parity)) return true;
         const long long t0 = clock64();
         for (;;) {
             if (ptx::mbar_try_wait_sleep(bar(i), parity)) return true;
             if (*abort) return false;
-            if (clock64() - t0 > kWaitLimit) {
+            if (clock64() - t0 > limit) {
                 *abort = 1;
                 raise_error(err, JANO_ETIMEOUT);
                 return false;
             }
         }
     }
-    __device__ bool poll(int i, uint32_t parity) const {
+    __device__ bool poll(int i, uint32_t parity, long long limit = kWaitLimit) const {
         if (ptx::mbar_try_wait(bar(i), parity)) return true;
         const long long t0 = clock64();
         while (!ptx::mbar_try_wait(bar(i), parity)) {
             if (*abort) return false;
-            if (clock64() - t0 > kWaitLimit) {
+            if (clock64() - t0 > limit) {
                 *abort = 1;
                 raise_error(err, JANO_ETIMEOUT);
                 return false;
@@ -60,14 +67,14 @@ struct Ctl {
         return true;
     }
     // Warp-uniform: the .sync.aligned operations that follow never diverge.
-    __device__ bool warp_wait(int i, uint32_t parity) const {
+    __device__ bool warp_wait(int i, uint32_t parity, long long limit = kWaitLimit) const {
         int ok = 0;
-        if ((threadIdx.x & 31) == 0) ok = wait(i, parity) ? 1 : 0;
+        if ((threadIdx.x & 31) == 0) ok = wait(i, parity, limit) ? 1 : 0;
         return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
     }
-    __device__ bool warp_poll(int i, uint32_t parity) const {
+    __device__ bool warp_poll(int i, uint32_t parity, long long limit = kWaitLimit) const {
         int ok = 0;
-        if ((threadIdx.x & 31) == 0) ok = poll(i, parity) ? 1 : 0;
+        if ((threadIdx.x & 31) == 0) ok = poll(i, parity, limit) ? 1 : 0;
         return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
     }
 };
