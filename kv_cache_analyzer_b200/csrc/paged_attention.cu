@@ -28,9 +28,11 @@
 // (At most 32 packed rows per sequence: paged_decode.cu, where a call brings
 // a workspace.)
 //
-// Bound by the tensor core and the softmax together, and in long runs by the
-// card's power: 16,380 rows over 32,760 positions of 12 heads of 128, pages of
-// 128 places, 3,080 us, 1,070 TFLOP/s, as the contiguous kernel.  Smaller pages
+// Bound by the tensor core and the softmax together (58% of the cycles have an
+// MMA) and by the rounds of CTAs over the SMs, and in long runs the card's power
+// lowers the clock: 16,380 rows over 32,760 positions of 12 heads of 128, pages
+// of 128 places, call after call, 3,101 us, 1,063 TFLOP/s (the contiguous kernel
+// beside it 3,135 us, 1,052); after a pause 2,730 us.  Smaller pages
 // are more copies: 4,096 rows over 16,384 positions of 24 heads take 753 us
 // with pages of 256 places, 777 with 64, 818 with 16.
 //
@@ -50,8 +52,9 @@
 // which one MMA requires of both operands) and its sum l is taken before that
 // rounding.  The running maximum follows lazily: O is rescaled only when it
 // grows by more than 2^8, which keeps P within BF16's range either way.
-// Every wait is bounded; a CTA that gives up records JANO_ETIMEOUT, takes
-// part in the cluster's barriers, and the rows it shares are not written.
+// Every wait is bounded (the one that spans a CTA's key tiles by their number);
+// a CTA that gives up records JANO_ETIMEOUT, takes part in the cluster's
+// barriers, and the rows it shares are not written.
 #include <cmath>
 
 #include "paged_tile.cuh"
@@ -710,7 +713,8 @@ cudaError_t launch_paged_attention(const PagedAttentionCall& c, int* err, cudaSt
     // K/V of few heads in L2 (4,680 rows over 32,760 positions: 915 us, heads
     // first 1,048).  Several: all heads of the longest tiles first, so that the
     // last CTAs are short ones (eight sequences of 500 to 8,000 positions: 440
-    // us, tiles first 485; four images: 144 and 151).
+    // us, tiles first 485; the due sets of three images, after a pause: 144 and
+    // 151).
     a.heads_first = c.seqs->n_seqs > 1 && tiles <= 65535;
     return c.pool->d == 128 ? launch_hd<128>(c, a, (int)tiles, err, st) : launch_hd<64>(c, a, (int)tiles, err, st);
 }

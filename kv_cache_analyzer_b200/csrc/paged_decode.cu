@@ -22,7 +22,11 @@
 // and their other rows are zeros, kept around Q.  The same 32 sequences over
 // and over, at 1000 W: 480 us with M = 128 over whatever lay behind Q (SM clock
 // 1,080 MHz), 448 with zeros there (1,300), 424 with M = 64 (1,540); a plain
-// sum of as many bytes takes 408 (1,680).  Cold, 405 us: 6.9 TB/s.
+// sum of as many bytes takes 408 (1,680).  After a pause, 405 us: 6.9 TB/s.
+//
+// P is rounded to BF16 for P V as in paged_attention.cu.  Two BF16 terms of P
+// would cost no bytes here, but one more MMA a tile (the power counts, above),
+// and a row's precision would depend on the form that its call takes.
 //
 // 7 warps:  0, 1  softmax of streams 0 and 1 (even and odd key tiles; thread =
 // packed row.  Stream 1's operand starts R rows before Q, so its rows fall
@@ -39,8 +43,9 @@
 // are issued.  Letting them run on into the next made that 323 us, and long
 // sequences of d = 64 4.5% slower.
 //
-// Every wait is bounded.  The partial slots of a CTA are marked missing before
-// it starts, so that rows of a CTA that gave up are not written.
+// Every wait is bounded (those that span a segment by the longest one's tiles).
+// The partial slots of a CTA are marked missing before it starts, so that rows
+// of a CTA that gave up are not written.
 #include "paged_tile.cuh"
 
 namespace jano {

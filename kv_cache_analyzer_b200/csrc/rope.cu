@@ -20,9 +20,9 @@
 // same slots in every head and keeps its cos and sin in registers for the
 // whole row.
 //
-// 18,900 rows of 40 heads of 128 (387 MB): 61.6 us, 6.3 TB/s; Q, K and V of
-// 11,466 rows of 12 heads of 128 into the cache (211 MB): 35.1 us, 6.0 TB/s,
-// into pages 37.7 us; a few rows: 2.0 us, the launch.
+// 18,900 rows of 40 heads of 128 (387 MB): 61.5 us, 6.3 TB/s; Q, K and V of
+// 11,466 rows of 12 heads of 128 into the cache (211 MB): 35.6 us, 5.9 TB/s,
+// as many into pages 38.1 us; a few rows: 2.2 us, the launch.
 #include <cuda_bf16.h>
 
 #include "jano_common.cuh"
